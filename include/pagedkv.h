@@ -373,6 +373,72 @@ pkv_status paged_kv_decode_step_cascade(const void* q, const void* k_new, const 
                                         void* workspace, size_t workspace_bytes, pkv_dtype dtype,
                                         pkv_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions and the cache write of models that use them.  A pair
+ * (x0, x1) of a q or k head at position p turns by a = p * inv_freq[j]:
+ *     y0 = x0 c - x1 s,  y1 = x1 c + x0 s,  c = rope_scale cos a,  s = rope_scale sin a
+ * for the rotary_dim / 2 pairs of the head's first rotary_dim elements; the
+ * elements behind them are copied unchanged.  Angles are exact products taken
+ * modulo a turn (to about 1e-6 up to positions of 2^24), the rotation is fp32
+ * and every result is rounded once.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    PKV_ROPE_HALF = 0,        /* pairs (j, j + rotary_dim / 2) */
+    PKV_ROPE_INTERLEAVED = 1  /* pairs (2j, 2j + 1) */
+} pkv_rope_layout;
+
+typedef enum {
+    PKV_ROPE_SCALE_NONE = 0,
+    PKV_ROPE_SCALE_LINEAR = 1,  /* every frequency divided by factor */
+    PKV_ROPE_SCALE_NTK = 2,     /* the base raised by factor^(R / (R - 2)) */
+    PKV_ROPE_SCALE_YARN = 3     /* slow pairs divided by factor, fast ones kept, a ramp between */
+} pkv_rope_scaling;
+
+/* Host only: fills inv_freq[rotary_dim / 2] (host) with base^(-2j / rotary_dim)
+ * scaled for contexts `factor` (>= 1) times the original length, and
+ * *rope_scale with the factor on cos and sin (1, or 0.1 ln(factor) + 1 for
+ * YaRN).  original_max_position, beta_fast and beta_slow are read for YaRN
+ * only: pairs that turn more than beta_fast times over the original length
+ * keep their frequency, pairs that turn less than beta_slow times are divided.
+ * The caller copies the table to the device once. */
+pkv_status paged_kv_rope_frequencies(int rotary_dim, double base, pkv_rope_scaling scaling,
+                                     double factor, int original_max_position, double beta_fast,
+                                     double beta_slow, float* inv_freq, float* rope_scale);
+
+/* For each token t with slot = slot_mapping[t] >= 0: rotates the q heads of
+ * row t to positions[t] into q_out, the k heads into row `slot` of the K pool,
+ * and copies the v heads into the V pool.  slot < 0 marks a padding token and
+ * slot >= num_blocks * 16 a bad one (flagged): nothing of the token is written,
+ * its q_out row included.  Slots must be unique within a call.
+ *  q, k_new, v_new: rows of num_q_heads (num_kv_heads) heads of head_dim
+ *             elements, q_stride / k_stride / v_stride elements from token to
+ *             token (multiples of 8, at least a row: the parts of one
+ *             projection's rows are such views).
+ *  q_out:     [num_tokens][num_q_heads][head_dim]; q itself (contiguous), or
+ *             memory that shares no byte with q, k_new or v_new.
+ *  positions: [num_tokens] int32; inv_freq: [rotary_dim / 2] fp32, device.
+ * rotary_dim is even and at most head_dim; head_dim a multiple of 8 up to 512
+ * (else PKV_ERR_UNSUPPORTED). */
+pkv_status paged_kv_rope_write(const void* q, const void* k_new, const void* v_new,
+                               long long q_stride, long long k_stride, long long v_stride,
+                               const int32_t* positions, const int64_t* slot_mapping,
+                               const float* inv_freq, float rope_scale, int num_tokens,
+                               int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                               pkv_rope_layout layout, int num_blocks, void* q_out, void* k_cache,
+                               void* v_cache, pkv_dtype dtype, pkv_stream_t stream);
+
+/* paged_kv_rope_write for a decode step's new tokens: sequence s's token is at
+ * position context_lens[s] - 1, in the slot that paged_kv_slot_mapping gives.
+ * A sequence of length 0, or with a bad length or table entry (flagged), is
+ * left alone.  slot_mapping_out: [num_seqs] int64, device, or NULL. */
+pkv_status paged_kv_rope_write_new_tokens(
+    const void* q, const void* k_new, const void* v_new, long long q_stride, long long k_stride,
+    long long v_stride, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, const float* inv_freq, float rope_scale, int num_seqs,
+    int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim, pkv_rope_layout layout,
+    int num_blocks, void* q_out, void* k_cache, void* v_cache, int64_t* slot_mapping_out,
+    pkv_dtype dtype, pkv_stream_t stream);
+
 /* Chunked-prefill attention over the paged cache ([P2] 使用教程 step 4 and
  * 核心亮点: a self-written FlashAttention serves the prefill stage; [P3]
  * §关键工程决策 item 2: prefill chunks are batched with decode).  Sequence s

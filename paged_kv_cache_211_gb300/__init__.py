@@ -28,6 +28,7 @@ __all__ = [
     "paged_kv_last_error", "pkv_selftest_bounded_wait",
     "BlockAllocator", "new_workspace", "paged_kv_block_hash", "paged_kv_copy_blocks",
     "paged_attention_decode_noalloc", "paged_attention_noalloc_scratch_bytes",
+    "paged_kv_rope_frequencies", "paged_kv_rope_write", "paged_kv_rope_write_new_tokens",
     "PKV_OK", "PKV_ERR_INVALID_ARG", "PKV_ERR_UNSUPPORTED", "PKV_ERR_NO_BLOCKS",
     "PKV_ERR_BAD_BLOCK_ID", "PKV_ERR_CUDA", "PKV_ERR_WORKSPACE",
 ]
@@ -55,6 +56,7 @@ class PagedKVError(RuntimeError):
 _lib = None
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll, _d = ctypes.c_longlong, ctypes.c_double
 _SIGS = {
     "pkv_version": ([], _i),
     "pkv_status_string": ([_i], ctypes.c_char_p),
@@ -110,6 +112,11 @@ _SIGS = {
     "paged_attention_decode_noalloc": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f,
                                         _vp, _i, _vp], _i),
     "paged_attention_noalloc_scratch_bytes": ([], _sz),
+    "paged_kv_rope_frequencies": ([_i, _d, _i, _d, _i, _d, _d, _vp, ctypes.POINTER(_f)], _i),
+    "paged_kv_rope_write": ([_vp, _vp, _vp, _ll, _ll, _ll, _vp, _vp, _vp, _f, _i, _i, _i, _i, _i,
+                             _i, _i, _vp, _vp, _vp, _i, _vp], _i),
+    "paged_kv_rope_write_new_tokens": ([_vp, _vp, _vp, _ll, _ll, _ll, _vp, _i, _vp, _vp, _f, _i,
+                                        _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp], _i),
 }
 
 
@@ -515,6 +522,102 @@ def paged_kv_copy_blocks(k_cache, v_cache, src_block_ids, dst_block_ids, stream=
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(src_block_ids, "src"),
         _dev(dst_block_ids, "dst"), src_block_ids.numel(), NB, Hkv, D, _dtype_code(k_cache),
         _stream(stream)))
+
+
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def paged_kv_rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0,
+                              original_max_position=0, beta_fast=32.0, beta_slow=1.0,
+                              device="cpu"):
+    """(inv_freq fp32 [rotary_dim / 2] on `device`, rope_scale) of a context scaling:
+    "none", "linear", "ntk" or "yarn".  Computed on the host; keep the table."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}")
+    inv_freq = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float32)
+    rope_scale = ctypes.c_float(0.0)
+    _check("paged_kv_rope_frequencies", lib().paged_kv_rope_frequencies(
+        int(rotary_dim), float(base), _ROPE_SCALINGS[scaling], float(factor),
+        int(original_max_position), float(beta_fast), float(beta_slow),
+        ctypes.c_void_p(inv_freq.data_ptr()), ctypes.byref(rope_scale)))
+    return inv_freq.to(device), rope_scale.value
+
+
+def _one_device(**tensors):
+    """All given tensors on the current CUDA device (the kernels launch there)."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    dev = torch.device("cuda", torch.cuda.current_device())
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current device {dev}")
+
+
+def _rows(t: torch.Tensor, name: str):
+    """Pointer and token stride of rows [T, heads, D] whose heads are packed (the
+    tokens may be spaced, as in a view of a wider projection's rows)."""
+    T, H, D = t.shape
+    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name} must have contiguous heads (only the token stride is free)")
+    stride = t.stride(0) if T > 1 else -(-H * D // 8) * 8
+    if stride < H * D:
+        raise ValueError(f"{name}'s tokens must not overlap")
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def _check_rope(q, k_new, v_new, k_cache, v_cache, inv_freq, q_out):
+    T, Hq, D = q.shape
+    NB, bs, Hkv, D2 = k_cache.shape
+    if bs != BLOCK_SIZE or D2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("pool shape must be [num_blocks, 16, num_kv_heads, head_dim]")
+    _check_new_rows(k_new, v_new, (T, Hkv, D), q.dtype)
+    _check_dtypes(q, k_cache, v_cache, q_out)
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or 2 * inv_freq.numel() > D:
+        raise ValueError("inv_freq must be float32 [rotary_dim / 2], rotary_dim <= head_dim")
+    return T, Hq, Hkv, D, NB
+
+
+def paged_kv_rope_write(q, k_new, v_new, k_cache, v_cache, positions, slot_mapping, inv_freq,
+                        q_out, interleaved=False, rope_scale=1.0, stream=None):
+    """Rotate q [T, Hq, D] to `positions` into q_out and k_new [T, Hkv, D] into its slots of the
+    K pool, and copy v_new into the V pool; tokens with slot -1 are left alone.
+    The rotary dim is 2 * len(inv_freq); q_out may be q; q, k_new and v_new may be
+    views of one projection's rows.  Returns q_out."""
+    T, Hq, Hkv, D, NB = _check_rope(q, k_new, v_new, k_cache, v_cache, inv_freq, q_out)
+    if positions.dtype != torch.int32 or positions.numel() != T:
+        raise ValueError("positions must be int32 [num_tokens]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
+    _one_device(q=q, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
+                positions=positions, slot_mapping=slot_mapping, inv_freq=inv_freq, q_out=q_out)
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k_new, "k_new"), _rows(v_new, "v_new")
+    _check("paged_kv_rope_write", lib().paged_kv_rope_write(
+        qp, kp, vp, qs, ks, vs, _dev(positions, "positions"), _dev(slot_mapping, "slot_mapping"),
+        _dev(inv_freq, "inv_freq"), float(rope_scale), T, Hq, Hkv, D, 2 * inv_freq.numel(),
+        int(bool(interleaved)), NB, _dev(q_out, "q_out"), _dev(k_cache, "k_cache"),
+        _dev(v_cache, "v_cache"), _dtype_code(q), _stream(stream)))
+    return q_out
+
+
+def paged_kv_rope_write_new_tokens(q, k_new, v_new, k_cache, v_cache, block_tables, context_lens,
+                                   inv_freq, q_out, interleaved=False, rope_scale=1.0,
+                                   slot_mapping_out=None, stream=None):
+    """paged_kv_rope_write of a decode step's tokens: each sequence's at position len-1."""
+    B, Hq, Hkv, D, NB = _check_rope(q, k_new, v_new, k_cache, v_cache, inv_freq, q_out)
+    _check_tables(block_tables, context_lens, B)
+    _check_slots(slot_mapping_out, B, "slot_mapping_out")
+    _one_device(q=q, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
+                block_tables=block_tables, context_lens=context_lens, inv_freq=inv_freq,
+                q_out=q_out, slot_mapping_out=slot_mapping_out)
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k_new, "k_new"), _rows(v_new, "v_new")
+    _check("paged_kv_rope_write_new_tokens", lib().paged_kv_rope_write_new_tokens(
+        qp, kp, vp, qs, ks, vs, _dev(block_tables, "block_tables"), block_tables.shape[1],
+        _dev(context_lens, "context_lens"), _dev(inv_freq, "inv_freq"), float(rope_scale), B, Hq,
+        Hkv, D, 2 * inv_freq.numel(), int(bool(interleaved)), NB, _dev(q_out, "q_out"),
+        _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+        _opt(slot_mapping_out, "slot_mapping_out"), _dtype_code(q), _stream(stream)))
+    return q_out
 
 
 def pkv_device_status(reset: bool = True) -> int:
