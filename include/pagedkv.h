@@ -439,6 +439,43 @@ pkv_status paged_kv_rope_write_new_tokens(
     int num_blocks, void* q_out, void* k_cache, void* v_cache, int64_t* slot_mapping_out,
     pkv_dtype dtype, pkv_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention with modified scores.  For the query of head i at position p of
+ * sequence s and the key at position t:
+ *     z = scale * <q, k_t>
+ *     z = softcap * tanh(z / softcap)          if softcap > 0
+ *     z = z - alibi_slopes[i] * |p - t|        if alibi_slopes
+ * over the visible keys
+ *     max(0, key_starts[s], p - window + 1) <= t < max(p + 1, min(prefix_lens[s], n))
+ * (n = context_lens[s]; window 0, key_starts NULL and prefix_lens NULL leave
+ * their term out), out = softmax(z) V.  A query that sees no key gives zeros.
+ * alibi_slopes: [num_q_heads] fp32; key_starts, prefix_lens: [num_seqs] int32
+ * (negative counts as 0), all device.  softcap and window are >= 0.
+ * key_starts is also how documents packed into one cached sequence are kept
+ * apart: each is an entry of its own (its query rows, its length, the shared
+ * table row) that starts at its document's first key.
+ * Only table entries of blocks with a key some query of the sequence sees are
+ * read, so blocks that slid out of the window may have been freed.  K and V of
+ * keys that a query does not see never reach its output, NaN included.
+ * ------------------------------------------------------------------------- */
+size_t paged_attention_decode_scored_workspace_bytes(int num_seqs, int num_q_heads,
+                                                     int num_kv_heads, int head_dim,
+                                                     int max_context_len);
+
+/* paged_attention_decode with modified scores: one query per sequence, at
+ * position context_lens[s] - 1.  max_context_len, out, the errors and the
+ * device checks are as there; workspace: 256-byte aligned, at least
+ * paged_attention_decode_scored_workspace_bytes(...), no initialisation, one
+ * call at a time (calls in one stream, or graphs that never run together).
+ * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads in 1..8, num_seqs
+ * <= 8192; else PKV_ERR_UNSUPPORTED. */
+pkv_status paged_attention_decode_scored(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* context_lens, int max_context_len, int num_seqs,
+    int num_q_heads, int num_kv_heads, int head_dim, int num_blocks, float scale, float softcap,
+    const float* alibi_slopes, int window, const int32_t* key_starts, void* out, void* workspace,
+    size_t workspace_bytes, pkv_dtype dtype, pkv_stream_t stream);
+
 /* Chunked-prefill attention over the paged cache ([P2] 使用教程 step 4 and
  * 核心亮点: a self-written FlashAttention serves the prefill stage; [P3]
  * §关键工程决策 item 2: prefill chunks are batched with decode).  Sequence s

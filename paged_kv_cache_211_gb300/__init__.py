@@ -29,6 +29,8 @@ __all__ = [
     "BlockAllocator", "new_workspace", "paged_kv_block_hash", "paged_kv_copy_blocks",
     "paged_attention_decode_noalloc", "paged_attention_noalloc_scratch_bytes",
     "paged_kv_rope_frequencies", "paged_kv_rope_write", "paged_kv_rope_write_new_tokens",
+    "paged_attention_decode_scored_workspace_bytes", "new_scored_workspace",
+    "paged_attention_decode_scored",
     "PKV_OK", "PKV_ERR_INVALID_ARG", "PKV_ERR_UNSUPPORTED", "PKV_ERR_NO_BLOCKS",
     "PKV_ERR_BAD_BLOCK_ID", "PKV_ERR_CUDA", "PKV_ERR_WORKSPACE",
 ]
@@ -117,6 +119,9 @@ _SIGS = {
                              _i, _i, _vp, _vp, _vp, _i, _vp], _i),
     "paged_kv_rope_write_new_tokens": ([_vp, _vp, _vp, _ll, _ll, _ll, _vp, _i, _vp, _vp, _f, _i,
                                         _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp], _i),
+    "paged_attention_decode_scored_workspace_bytes": ([_i, _i, _i, _i, _i], _sz),
+    "paged_attention_decode_scored": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f,
+                                       _f, _vp, _i, _vp, _vp, _vp, _sz, _i, _vp], _i),
 }
 
 
@@ -618,6 +623,51 @@ def paged_kv_rope_write_new_tokens(q, k_new, v_new, k_cache, v_cache, block_tabl
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
         _opt(slot_mapping_out, "slot_mapping_out"), _dtype_code(q), _stream(stream)))
     return q_out
+
+
+def paged_attention_decode_scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                  max_context_len) -> int:
+    return lib().paged_attention_decode_scored_workspace_bytes(
+        num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len)
+
+
+def new_scored_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                         device) -> torch.Tensor:
+    """A workspace tensor for paged_attention_decode_scored (caller-owned)."""
+    n = paged_attention_decode_scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads,
+                                                      head_dim, max_context_len)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _check_score_mods(Hq, B, alibi_slopes, **per_seq):
+    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32
+                                     or alibi_slopes.numel() != Hq):
+        raise ValueError("alibi_slopes must be float32 [num_q_heads]")
+    for name, t in per_seq.items():
+        if t is not None and (t.dtype != torch.int32 or t.numel() != B):
+            raise ValueError(f"{name} must be int32 [num_seqs]")
+
+
+def paged_attention_decode_scored(q, k_cache, v_cache, block_tables, context_lens,
+                                  max_context_len, scale, out, workspace, softcap=0.0,
+                                  alibi_slopes=None, window=0, key_starts=None, stream=None):
+    """paged_attention_decode with capped (softcap * tanh(z / softcap)) and biased
+    (- slope * distance) scores, over the last `window` keys and those from
+    key_starts on.  workspace: new_scored_workspace()."""
+    B, Hq, Hkv, D, NB = _check_decode_shapes(q, k_cache, v_cache, block_tables, context_lens,
+                                             out)
+    _check_score_mods(Hq, B, alibi_slopes, key_starts=key_starts)
+    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                context_lens=context_lens, out=out, workspace=workspace,
+                alibi_slopes=alibi_slopes, key_starts=key_starts)
+    _check("paged_attention_decode_scored", lib().paged_attention_decode_scored(
+        _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+        _dev(block_tables, "block_tables"), block_tables.shape[1],
+        _dev(context_lens, "context_lens"), int(max_context_len), B, Hq, Hkv, D, NB,
+        float(scale), float(softcap), _opt(alibi_slopes, "alibi_slopes"), int(window),
+        _opt(key_starts, "key_starts"), _dev(out, "out"), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream)))
+    return out
 
 
 def pkv_device_status(reset: bool = True) -> int:
