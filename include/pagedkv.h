@@ -476,6 +476,26 @@ pkv_status paged_attention_decode_scored(
     const float* alibi_slopes, int window, const int32_t* key_starts, void* out, void* workspace,
     size_t workspace_bytes, pkv_dtype dtype, pkv_stream_t stream);
 
+/* paged_attention_prefill with modified scores: packed query chunks, the rows
+ * of sequence s at positions context_lens[s] - q_len[s] .. context_lens[s] - 1.
+ * prefix_lens makes the first tokens of a sequence visible to every row (a
+ * bidirectional prefix; those keys must be in the cache, and the part of a
+ * prefix past context_lens[s] does not count).  Chunks, bounds, flags and
+ * skipped sequences are as in paged_attention_prefill.  workspace: as for
+ * paged_attention_decode_scored, of
+ * paged_attention_prefill_scored_workspace_bytes(...) bytes (where items are
+ * few, each is cut into runs of keys that are joined by a second kernel).
+ * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads up to 16. */
+size_t paged_attention_prefill_scored_workspace_bytes(int num_seqs, int max_q_len, int num_q_heads,
+                                                      int num_kv_heads, int head_dim);
+pkv_status paged_attention_prefill_scored(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* context_lens, const int32_t* cu_q_lens, int num_seqs,
+    int max_q_len, int num_q_rows, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+    float scale, float softcap, const float* alibi_slopes, int window, const int32_t* key_starts,
+    const int32_t* prefix_lens, void* out, void* workspace, size_t workspace_bytes,
+    pkv_dtype dtype, pkv_stream_t stream);
+
 /* Chunked-prefill attention over the paged cache ([P2] 使用教程 step 4 and
  * 核心亮点: a self-written FlashAttention serves the prefill stage; [P3]
  * §关键工程决策 item 2: prefill chunks are batched with decode).  Sequence s

@@ -30,7 +30,8 @@ __all__ = [
     "paged_attention_decode_noalloc", "paged_attention_noalloc_scratch_bytes",
     "paged_kv_rope_frequencies", "paged_kv_rope_write", "paged_kv_rope_write_new_tokens",
     "paged_attention_decode_scored_workspace_bytes", "new_scored_workspace",
-    "paged_attention_decode_scored",
+    "paged_attention_decode_scored", "paged_attention_prefill_scored_workspace_bytes",
+    "new_prefill_scored_workspace", "paged_attention_prefill_scored",
     "PKV_OK", "PKV_ERR_INVALID_ARG", "PKV_ERR_UNSUPPORTED", "PKV_ERR_NO_BLOCKS",
     "PKV_ERR_BAD_BLOCK_ID", "PKV_ERR_CUDA", "PKV_ERR_WORKSPACE",
 ]
@@ -122,6 +123,10 @@ _SIGS = {
     "paged_attention_decode_scored_workspace_bytes": ([_i, _i, _i, _i, _i], _sz),
     "paged_attention_decode_scored": ([_vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f,
                                        _f, _vp, _i, _vp, _vp, _vp, _sz, _i, _vp], _i),
+    "paged_attention_prefill_scored_workspace_bytes": ([_i, _i, _i, _i, _i], _sz),
+    "paged_attention_prefill_scored": ([_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                        _i, _f, _f, _vp, _i, _vp, _vp, _vp, _vp, _sz, _i, _vp],
+                                       _i),
 }
 
 
@@ -666,6 +671,50 @@ def paged_attention_decode_scored(q, k_cache, v_cache, block_tables, context_len
         _dev(context_lens, "context_lens"), int(max_context_len), B, Hq, Hkv, D, NB,
         float(scale), float(softcap), _opt(alibi_slopes, "alibi_slopes"), int(window),
         _opt(key_starts, "key_starts"), _dev(out, "out"), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream)))
+    return out
+
+
+def paged_attention_prefill_scored_workspace_bytes(num_seqs, max_q_len, num_q_heads,
+                                                   num_kv_heads, head_dim) -> int:
+    return lib().paged_attention_prefill_scored_workspace_bytes(num_seqs, max_q_len, num_q_heads,
+                                                                num_kv_heads, head_dim)
+
+
+def new_prefill_scored_workspace(num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
+                                 device) -> torch.Tensor:
+    """A workspace tensor for paged_attention_prefill_scored (caller-owned)."""
+    n = paged_attention_prefill_scored_workspace_bytes(num_seqs, max_q_len, num_q_heads,
+                                                       num_kv_heads, head_dim)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def paged_attention_prefill_scored(q, k_cache, v_cache, block_tables, context_lens, cu_q_lens,
+                                   max_q_len, scale, out, workspace, softcap=0.0,
+                                   alibi_slopes=None, window=0, key_starts=None,
+                                   prefix_lens=None, stream=None):
+    """paged_attention_prefill with capped and biased scores, windows, key starts
+    (documents) and bidirectional prefixes.  workspace: new_prefill_scored_workspace()."""
+    R, Hq, D = q.shape
+    NB, bs, Hkv, D2 = k_cache.shape
+    if bs != BLOCK_SIZE or D2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("pool shape must be [num_blocks, 16, num_kv_heads, head_dim]")
+    B = context_lens.numel()
+    _check_tables(block_tables, context_lens, B)
+    if cu_q_lens.dtype != torch.int32 or cu_q_lens.numel() != B + 1:
+        raise ValueError("cu_q_lens must be int32 [num_seqs + 1]")
+    _check_dtypes(q, k_cache, v_cache, out)
+    _check_score_mods(Hq, B, alibi_slopes, key_starts=key_starts, prefix_lens=prefix_lens)
+    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                context_lens=context_lens, cu_q_lens=cu_q_lens, out=out, workspace=workspace,
+                alibi_slopes=alibi_slopes, key_starts=key_starts, prefix_lens=prefix_lens)
+    _check("paged_attention_prefill_scored", lib().paged_attention_prefill_scored(
+        _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+        _dev(block_tables, "block_tables"), block_tables.shape[1],
+        _dev(context_lens, "context_lens"), _dev(cu_q_lens, "cu_q_lens"), B, int(max_q_len), R,
+        Hq, Hkv, D, NB, float(scale), float(softcap), _opt(alibi_slopes, "alibi_slopes"),
+        int(window), _opt(key_starts, "key_starts"), _opt(prefix_lens, "prefix_lens"),
+        _dev(out, "out"), _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream)))
     return out
 

@@ -1,0 +1,1033 @@
+// pkv_scored_prefill.cu -- chunked-prefill attention with capped or biased
+// scores over windows, prefixes and documents (pkv_scored.cuh has the score
+// and the visible keys; a row's keys are one interval [lo, hi)).
+//
+// Each visible (row, key) pair costs 4 D flop in two matrix products, run as
+// tcgen05.mma with fp32 accumulators in tensor memory, and one score through
+// cap, bias and exp2.  With a cap the scores, not the products, bound it: the
+// special-function pipe does tanh as exp2 and a reciprocal, three results a
+// score with the softmax's own exp2.  So a tile whose scores all lie within
+// |z / cap| <= 0.75 takes tanh from a polynomial on the (packed, two a cycle)
+// fp32 pipe instead, and only the others from exp2 and the reciprocal.
+//
+// Work item: one sequence, one KV head, a pair of 128-row tiles A and B (256
+// consecutive (query token, query head) rows) and, where items are few, one of
+// `splits` runs of its key tiles.  Key tiles are 128 keys (8 blocks), counted
+// from the first block that a row of the item sees.  A persistent CTA per SM:
+//   warp 0 / 3   tensor copies of the K / V blocks into two-stage rings,
+//   warp 2       tensor memory; the Q tiles,
+//   warp 1       (one thread) S_X = Q_X K^T and O_X += P_X V, ordered
+//                ... PV_A(J), S_A(J+1), PV_B(J), S_B(J+1) ..., so the tensor
+//                core works on one tile while the other's softmax runs,
+//   warps 4-7 / 8-11  the scores of tile A / B, one thread a row: 128 scores
+//                in registers, cap, bias, mask (a select), running maximum
+//                and sum, P as 16-bit values over the scores.
+// An item whose rows fill tile A only leaves tile B out.  O is rescaled only
+// when a row's maximum grows by more than 2^8.  V rows that no row of the item
+// sees are zeroed before P V.  Rows of one tile see different keys, so a
+// hidden key's NaN or infinity in V would still meet a zero weight: a row
+// whose O is not finite is computed again, by a plain loop over its own keys.
+// Every wait is bounded.
+#include <cstdlib>
+#include <type_traits>
+
+#include "pkv_scored.cuh"
+#include "pkv_tc.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRows = 128;             // rows of a tile
+constexpr int kPair = 2 * kRows;       // rows of an item
+constexpr int kKeys = 128;             // keys of a key tile
+constexpr int kTileBlocks = kKeys / PKV_BLOCK_SIZE;
+constexpr float kRescale = 8.f;        // log2 of the largest P before O is rescaled
+constexpr int kMaxCtas = 160;          // bounds the workspace of split items
+constexpr int kMaxGroup = 16;
+// Registers: launched at kLaunchRegs a thread (checked on the host); the load /
+// MMA warpgroup gives some up and the two softmax warpgroups take them.
+constexpr int kLaunchRegs = 168;
+constexpr int kOtherRegs = 88;
+constexpr int kSoftmaxRegs = 208;
+static_assert(128 * kOtherRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs,
+              "register shares exceed the launch total");
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// tanh(x) / x on |x| <= 0.75 as a polynomial in x^2: fitted here by iterated
+// weighted least squares to the smallest largest relative error, 5.7e-7.
+constexpr float kTanhRange = 0.75f;
+constexpr int kTanhTerms = 5;
+__host__ __device__ constexpr float tanh_term(int i) {
+    return i == 0 ? 0.999999435f : i == 1 ? -0.333282515f : i == 2 ? 0.132589832f : i == 3 ? -0.0500563026f : 0.0129296324f;
+}
+
+struct PrefillScored {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    void* out;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* cu_q_lens;
+    unsigned int* status;
+    ScoreMods mods;
+    int num_seqs, num_q_heads, num_kv_heads, group, max_blocks_per_seq, num_blocks;
+    int max_q_len, num_q_rows;
+    int pairs_per_seq;     // ceil(max_q_len * group / kPair)
+    int splits;            // key runs per item; > 1: partials go to the workspace
+    float tanh_c[kTanhTerms];  // the polynomial's terms in (raw score)^2
+    float tanh_limit;      // largest |raw score| it serves (negative: none)
+    // partials of split items: row = ((base item) * splits + split) * kPair + row of the pair
+    float* ws_m;
+    float* ws_l;
+    float* ws_o;           // [row][D]
+};
+
+struct Item {
+    int s, h, q0, qlen, n, row0;
+    int split, base;       // base: item without its split
+    int lo, hi;            // keys that some row of the item sees
+    int b0, nblk;          // this split's first block and its number of blocks
+    int nkv;               // its key tiles (0: nothing to compute)
+    bool has_b;            // tile B holds rows
+};
+
+// A sequence's chunk is usable if its rows lie inside q and out, it is no
+// longer than the host bound, and it fits its context and the table.
+__device__ __forceinline__ bool lengths_ok(const PrefillScored& p, int q0, int qlen, int n) {
+    return qlen > 0 && q0 >= 0 && q0 <= p.num_q_rows - qlen && qlen <= p.max_q_len && n >= qlen &&
+           n <= p.max_blocks_per_seq * PKV_BLOCK_SIZE;
+}
+
+// Keys hidden behind a prefix end at this bound for the query at position p.
+__device__ __forceinline__ int end_key(const ScoreMods& m, int s, int p, int n) {
+    const int pre = m.prefix_lens ? min(m.prefix_lens[s], n) : 0;
+    return max(p + 1, pre);
+}
+
+// Item i, heaviest first (pairs from the end of each chunk, where the causal
+// range is longest); false if it holds no rows or its lengths are invalid
+// (flagged once per sequence).
+__device__ __forceinline__ bool item_at(const PrefillScored& p, int i, bool flag, Item& it) {
+    const int per_pair = p.num_seqs * p.num_kv_heads * p.splits;
+    const int pair = p.pairs_per_seq - 1 - i / per_pair;
+    int rem = i % per_pair;
+    it.split = rem % p.splits;
+    rem /= p.splits;
+    it.s = rem / p.num_kv_heads;
+    it.h = rem - it.s * p.num_kv_heads;
+    it.base = (it.s * p.num_kv_heads + it.h) * p.pairs_per_seq + pair;
+    it.q0 = p.cu_q_lens[it.s];
+    it.qlen = p.cu_q_lens[it.s + 1] - it.q0;
+    it.n = p.context_lens[it.s];
+    if (!lengths_ok(p, it.q0, it.qlen, it.n)) {
+        if (flag && pair == 0 && it.h == 0 && it.split == 0 && it.qlen != 0)
+            atomicOr(p.status, PKV_DEV_BAD_LENGTH);
+        return false;
+    }
+    const int g = p.group, rows = it.qlen * g;
+    it.row0 = pair * kPair;
+    if (it.row0 >= rows) return false;
+    it.has_b = it.row0 + kRows < rows;
+    const int t_first = it.row0 / g;
+    const int t_last = min(it.qlen, (it.row0 + kPair + g - 1) / g) - 1;
+    const int base_pos = it.n - it.qlen;
+    it.lo = first_key(p.mods, it.s, base_pos + t_first);
+    it.hi = end_key(p.mods, it.s, base_pos + t_last, it.n);
+    it.b0 = it.lo / PKV_BLOCK_SIZE;
+    it.nblk = it.nkv = 0;
+    if (it.lo >= it.hi) return true;
+    const int blocks = (it.hi + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE - it.b0;
+    const int tiles = (blocks + kTileBlocks - 1) / kTileBlocks;
+    const int j0 = (int)((long long)tiles * it.split / p.splits);
+    const int j1 = (int)((long long)tiles * (it.split + 1) / p.splits);
+    it.nkv = j1 - j0;
+    it.b0 += j0 * kTileBlocks;
+    it.nblk = min(blocks - j0 * kTileBlocks, it.nkv * kTileBlocks);
+    return true;
+}
+
+// The item this CTA takes in round r: rounds alternate direction over the
+// CTAs, so that heaviest-first items even out.
+__device__ __forceinline__ int round_item(int r) {
+    const int G = gridDim.x, c = blockIdx.x;
+    return r * G + ((r & 1) ? G - 1 - c : c);
+}
+
+// Two-wide fp32 arithmetic on packed register pairs, the three-input maximum
+// and 32-byte stores.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(ptr),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                 "r"(w[7])
+                 : "memory");
+}
+
+// One row again, by a whole warp and from its own keys only (keys [lo, hi) of
+// its sequence): a key it does not see, or whose block id is bad, is never
+// read.  Lane x gets elements x * D / 32 .. of the unnormalised output.
+template <typename T, int D>
+__device__ __noinline__ void plain_row(const PrefillScored& p, int s, int h, int head, int row,
+                                       int pos, int lo, int hi, float (&o)[D / 32], float& m,
+                                       float& l) {
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    const T* q = static_cast<const T*>(p.q) + ((size_t)row * p.num_q_heads + head) * D;
+    const size_t stride = (size_t)p.num_kv_heads * D;
+    const T* kc = static_cast<const T*>(p.k_cache) + (size_t)h * D;
+    const T* vc = static_cast<const T*>(p.v_cache) + (size_t)h * D;
+    const int32_t* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+    const ScoreMods& md = p.mods;
+    const float slope = md.slopes ? md.slopes[head] * kScoreLog2e : 0.f;
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    for (int t0 = lo; t0 < hi; t0 += 32) {
+        const int t = t0 + lane;
+        int64_t slot = -1;
+        if (t < hi) {
+            const int id = table[t / PKV_BLOCK_SIZE];
+            if (id >= 0 && id < p.num_blocks)
+                slot = (int64_t)id * PKV_BLOCK_SIZE + t % PKV_BLOCK_SIZE;
+        }
+        float z = -INFINITY;
+        if (slot >= 0) {
+            float dot = 0.f;
+            const T* k = kc + slot * stride;
+            for (int d = 0; d < D; ++d) dot = fmaf((float)q[d], (float)k[d], dot);
+            z = md.cap_out > 0.f ? md.cap_out * tanhf(dot * md.cap_in) : dot * md.scale_log2;
+            z = fmaf(-slope, fabsf((float)(pos - t)), z);
+        }
+        float mx = z;
+        for (int off = 16; off > 0; off >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
+        const float f = fast_exp2(m - ms), w = slot >= 0 ? fast_exp2(z - ms) : 0.f;
+        m = mn;
+        float sum = w;
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        l = l * f + sum;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] *= f;
+        for (int x = 0; x < 32; ++x) {
+            const float wx = __shfl_sync(0xffffffffu, w, x);
+            const int64_t sx = __shfl_sync(0xffffffffu, slot, x);
+            if (sx < 0) continue;
+            const T* v = vc + sx * stride + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[e] = fmaf(wx, (float)v[e], o[e]);
+        }
+    }
+}
+
+template <typename T, int D, bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+    scored_prefill_kernel(const PrefillScored p, const __grid_constant__ CUtensorMap tmap_k,
+                          const __grid_constant__ CUtensorMap tmap_v,
+                          const __grid_constant__ CUtensorMap tmap_q, int q_tma, int num_items) {
+    using E = Elem<T>;
+    constexpr int HALVES = D / 64;
+    constexpr int REG = kRows * 128;       // one 64-element half of 128 rows: 16 KB
+    constexpr int TILE = HALVES * REG;     // a Q tile, or one K or V key tile
+    constexpr uint32_t kCols = 512;
+    constexpr uint32_t kOCol = 2 * kKeys;  // O_A at kOCol, O_B at kOCol + D
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    unsigned char* sq = smem_raw + (((raw + 1023u) & ~1023u) - raw);   // Q_A, Q_B
+    unsigned char* sk = sq + 2 * TILE;      // 2 stages
+    unsigned char* sv = sk + 2 * TILE;      // 2 stages
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sv + 2 * TILE);
+    uint64_t* k_full = bars + 0;            // [stage]
+    uint64_t* k_empty = bars + 2;
+    uint64_t* v_full = bars + 4;
+    uint64_t* v_empty = bars + 6;
+    uint64_t* q_full = bars + 8;            // [tile]
+    uint64_t* q_empty = bars + 10;
+    uint64_t* s_full = bars + 12;           // [tile]: S_X written
+    uint64_t* p_full = bars + 14;           // [tile]: its 4 softmax warps wrote P_X
+    uint64_t* o_ready = bars + 16;          // [tile]: an item's last P V_X done
+    uint64_t* o_free = bars + 18;           // [tile]: its softmax warps read O_X
+    uint64_t* mma_idle = bars + 20;
+    int* vbad = reinterpret_cast<int*>(bars + 21);           // [2] bad-block bits per V stage
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vbad + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = p.group, Hq = p.num_q_heads;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_ready[i], 1);
+            mbar_init(&o_free[i], 4);
+        }
+        mbar_init(mma_idle, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 2) tc_alloc(tmem_slot, kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int rounds = (num_items + (int)gridDim.x - 1) / (int)gridDim.x;
+    // whole warpgroups: warps 0-3 release registers, 4-11 take them
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------ K (warp 0) / V (warp 3) producers
+        const bool isk = warp == 0;
+        const CUtensorMap* map = isk ? &tmap_k : &tmap_v;
+        uint64_t* full = isk ? k_full : v_full;
+        uint64_t* empty = isk ? k_empty : v_empty;
+        unsigned char* ring = isk ? sk : sv;
+        int J = 0;  // key tiles issued by this CTA
+        bool live = true;
+        for (int rd = 0; rd < rounds && live; ++rd) {
+            const int i = round_item(rd);
+            Item it;
+            if (i >= num_items || !item_at(p, i, isk && lane == 0, it)) continue;
+            const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks_per_seq + it.b0;
+            for (int j = 0; j < it.nkv; ++j, ++J) {
+                const int b = J & 1, ph = (J >> 1) & 1;
+                live = __all_sync(0xffffffffu, mbar_wait(&empty[b], ph ^ 1, abort_flag, p.status));
+                if (!live) break;
+                const int nb = min(kTileBlocks, it.nblk - kTileBlocks * j);
+                int id = 0;
+                bool bad = false;
+                if (lane < nb) {
+                    id = table[kTileBlocks * j + lane];
+                    bad = id < 0 || id >= p.num_blocks;
+                    if (bad) id = 0;  // fetched, then masked and zeroed
+                }
+                const unsigned badm = __ballot_sync(0xffffffffu, bad);
+                if (lane == 0) {
+                    if (isk && badm) atomicOr(p.status, PKV_DEV_BAD_BLOCK_ID);
+                    if (!isk) vbad[b] = (int)badm;
+                    mbar_arrive_expect_tx(&full[b], (uint32_t)(nb * HALVES * 2048));
+                }
+                __syncwarp();
+                if (lane < nb) {
+#pragma unroll
+                    for (int hh = 0; hh < HALVES; ++hh)
+                        tma_load_rows(ring + b * TILE + hh * REG + lane * 2048, map, &full[b],
+                                      hh * 64, it.h, id * PKV_BLOCK_SIZE);
+                }
+            }
+        }
+        // every copy issued must land before the CTA may exit
+        if (lane == 0)
+            for (int j = max(0, J - 2); j < J; ++j) mbar_drain(&full[j & 1], (j >> 1) & 1, p.status);
+    } else if (warp == 2) {
+        // ------------------------------------------------------ Q tiles of each item
+        // By tensor copies (lane 0) where the group divides the tile's 128
+        // rows, else row by row (cp.async).  Rows past the chunk belong to the
+        // next one (or read as zeros): they are never stored.
+        const T* qb = static_cast<const T*>(p.q);
+        constexpr int CH = D / 8;  // 16-byte chunks per row
+        int issued[2] = {0, 0};    // items whose tile X was loaded
+        bool live = true;
+        for (int rd = 0; rd < rounds && live; ++rd) {
+            const int i = round_item(rd);
+            Item it;
+            if (i >= num_items || !item_at(p, i, false, it) || it.nkv == 0) continue;
+            for (int X = 0; X < (it.has_b ? 2 : 1) && live; ++X) {
+                live = __all_sync(0xffffffffu, mbar_wait(&q_empty[X], (issued[X] & 1) ^ 1,
+                                                         abort_flag, p.status));
+                if (!live) break;
+                ++issued[X];
+                const int row = it.row0 + X * kRows;
+                if (q_tma) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&q_full[X], (uint32_t)TILE);
+#pragma unroll
+                        for (int hh = 0; hh < HALVES; ++hh)
+                            tma_load_rows(sq + X * TILE + hh * REG, &tmap_q, &q_full[X], hh * 64,
+                                          it.h * g, it.q0 + row / g);
+                    }
+                    __syncwarp();
+                    continue;
+                }
+                for (int x = lane; x < kRows * CH; x += 32) {
+                    const int r = x / CH, c = x - r * CH;
+                    const int t = (row + r) / g;
+                    const bool in = t < it.qlen;
+                    const T* src = qb + ((size_t)(it.q0 + (in ? t : 0)) * Hq + it.h * g +
+                                         (in ? row + r - t * g : 0)) * D + c * 8;
+                    const uint32_t dst = smem_addr(sq + X * TILE + (c >> 3) * REG + r * 128 +
+                                                   (((c & 7) ^ (r & 7)) << 4));
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst),
+                                 "l"(src), "r"(in ? 16 : 0)
+                                 : "memory");
+                }
+                asm volatile("cp.async.commit_group;\n" ::: "memory");
+                asm volatile("cp.async.wait_all;\n" ::: "memory");
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[X]);
+            }
+        }
+        // every copy issued must land before the CTA may exit
+        if (q_tma && lane == 0)
+            for (int X = 0; X < 2; ++X)
+                if (issued[X] > 0) mbar_drain(&q_full[X], (issued[X] - 1) & 1, p.status);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+            const uint32_t id_s = tc_idesc_f16(kBf16, kRows, kKeys, 0, 0);
+            const uint32_t id_pv = tc_idesc_f16(kBf16, kRows, D, 0, 1);
+            const uint32_t aq = smem_addr(sq), ak = smem_addr(sk), av = smem_addr(sv);
+            // a cursor over the key tiles of this CTA's items, in order; per
+            // tile X the items and key tiles it took part in
+            struct Cur {
+                int r, j, J, nkv;
+                int items[2], tiles[2];
+                bool has_b;
+            };
+            auto advance = [&](Cur& c) -> bool {
+                if (c.r >= 0 && ++c.j < c.nkv) {
+                    ++c.J;
+                    ++c.tiles[0];
+                    if (c.has_b) ++c.tiles[1];
+                    return true;
+                }
+                for (++c.r; c.r < rounds; ++c.r) {
+                    const int i = round_item(c.r);
+                    Item it;
+                    if (i >= num_items || !item_at(p, i, false, it) || it.nkv == 0) continue;
+                    c.nkv = it.nkv;
+                    c.has_b = it.has_b;
+                    c.j = 0;
+                    ++c.J;
+                    ++c.items[0];
+                    ++c.tiles[0];
+                    if (c.has_b) {
+                        ++c.items[1];
+                        ++c.tiles[1];
+                    }
+                    return true;
+                }
+                return false;
+            };
+            // S_X(c) = Q_X K(c)^T into tile X's score buffer, over the last
+            // P_X, whose P V this thread issued before (MMAs run in order)
+            auto issue_s = [&](const Cur& c, int X) -> bool {
+                const int b = c.J & 1;
+                if (X == 0 && !mbar_wait(&k_full[b], (c.J >> 1) & 1, abort_flag, p.status))
+                    return false;
+                if (c.j == 0 && !mbar_wait(&q_full[X], c.items[X] & 1, abort_flag, p.status))
+                    return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma(tmem + X * kKeys,
+                           tc_smem_desc(aq + X * TILE + (ks >> 2) * REG + (ks & 3) * 32, 16, 1024),
+                           tc_smem_desc(ak + b * TILE + (ks >> 2) * REG + (ks & 3) * 32, 16, 1024),
+                           id_s, ks > 0);
+                tc_commit(&s_full[X]);
+                if (X == 1 || !c.has_b) tc_commit(&k_empty[b]);
+                if (c.j == c.nkv - 1) tc_commit(&q_empty[X]);
+                return true;
+            };
+            // O_X += P_X(c) V(c): P_X over the first 64 columns of its scores
+            auto issue_pv = [&](const Cur& c, int X) -> bool {
+                const int b = c.J & 1;
+                if (X == 0 && !mbar_wait(&v_full[b], (c.J >> 1) & 1, abort_flag, p.status))
+                    return false;
+                // the item's first P V overwrites O_X: the last item's must have been read
+                if (c.j == 0 && c.items[X] >= 1 &&
+                    !mbar_wait(&o_free[X], (c.items[X] - 1) & 1, abort_flag, p.status))
+                    return false;
+                if (!mbar_wait(&p_full[X], c.tiles[X] & 1, abort_flag, p.status)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    tc_mma_tmem_a(tmem + kOCol + X * D, tmem + X * kKeys + 8 * kk,
+                                  tc_smem_desc(av + b * TILE + kk * 2048, REG, 1024), id_pv,
+                                  c.j > 0 || kk > 0);
+                if (X == 1 || !c.has_b) tc_commit(&v_empty[b]);
+                if (c.j == c.nkv - 1) tc_commit(&o_ready[X]);
+                return true;
+            };
+            Cur cs = {-1, 0, -1, 0, {-1, -1}, {-1, -1}, false}, cp = cs;
+            bool live = true;
+            bool more = advance(cs);
+            if (more) live = issue_s(cs, 0) && (!cs.has_b || issue_s(cs, 1));
+            while (live && advance(cp)) {
+                more = advance(cs);
+                live = issue_pv(cp, 0);
+                if (live && more) live = issue_s(cs, 0);
+                if (live && cp.has_b) live = issue_pv(cp, 1);
+                if (live && more && cs.has_b) live = issue_s(cs, 1);
+            }
+            // nothing of this thread's may still run when tensor memory is freed
+            tc_commit(mma_idle);
+            mbar_drain(mma_idle, 0, p.status);
+        }
+        __syncwarp();
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+        // ---------------- scores of tile X (warps 4-7: A, 8-11: B), one thread per row
+        const int X = (warp - 4) >> 2;
+        const int wq = warp & 3;                             // tensor-memory lane quarter
+        const int r = 32 * wq + lane;                        // row of the tile
+        const uint32_t trow = tmem + ((uint32_t)(32 * wq) << 16);
+        const uint32_t sx = trow + X * kKeys;                // this tile's scores / P
+        const uint32_t ox = trow + kOCol + X * D;            // this tile's O
+        const ScoreMods& md = p.mods;
+        const float sl2 = md.scale_log2;
+        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+        int J = 0;             // key tiles of the CTA (the rings' count)
+        int items = 0, tiles = 0;  // items and key tiles of this tile X
+        bool ok = true;
+        for (int rd = 0; rd < rounds && ok; ++rd) {
+            const int i = round_item(rd);
+            Item it;
+            if (i >= num_items || !item_at(p, i, false, it)) continue;
+            if (X == 1 && !it.has_b) {
+                J += it.nkv;
+                continue;
+            }
+            const int R = it.row0 + X * kRows + r, t = R / g;
+            const bool live_row = t < it.qlen;
+            const int head = it.h * g + (live_row ? R - t * g : 0);
+            const int pos = it.n - it.qlen + (live_row ? t : 0);
+            // this row's visible keys (rows past the chunk: everything, never stored)
+            const int lo = live_row ? first_key(md, it.s, pos) : 0;
+            const int hi = live_row ? end_key(md, it.s, pos, it.n) : 0x7fffffff;
+            const float slope2 = kBias ? md.slopes[head] * kScoreLog2e : 0.f;
+            float m_used = -INFINITY, l = 0.f;
+            for (int j = 0; j < it.nkv; ++j, ++J, ++tiles) {
+                const int b = J & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[X], tiles & 1, abort_flag, p.status));
+                if (!ok) break;
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&v_full[b], (J >> 1) & 1, abort_flag, p.status));
+                if (!ok) break;
+                tc_fence_after();
+                const unsigned bad = (unsigned)vbad[b];              // 8 blocks of the tile
+                const int key0 = it.b0 * PKV_BLOCK_SIZE + kKeys * j;
+                const bool whole = bad == 0u && __all_sync(0xffffffffu, key0 >= lo &&
+                                                                            key0 + kKeys <= hi);
+                float sc[kKeys];
+#pragma unroll
+                for (int q4 = 0; q4 < kKeys / 32; ++q4)
+                    tc_ld32(sx + 32 * q4, reinterpret_cast<uint32_t(&)[32]>(sc[32 * q4]));
+                tc_wait_ld();
+                // sc becomes z / mul (base-2 scores z): raw scores, or
+                // raw * tanh(x) / x with x = raw * cap_in, or z itself
+                float mul = sl2;
+                if constexpr (kCap) {
+                    float ab[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < kKeys; c += 2)
+                        ab[(c >> 1) & 3] = max3(ab[(c >> 1) & 3], fabsf(sc[c]), fabsf(sc[c + 1]));
+                    const float big = fmaxf(fmaxf(ab[0], ab[1]), fmaxf(ab[2], ab[3]));
+                    if (__all_sync(0xffffffffu, big <= p.tanh_limit)) {
+                        uint64_t tc[kTanhTerms];
+#pragma unroll
+                        for (int k = 0; k < kTanhTerms; ++k) tc[k] = f2(p.tanh_c[k], p.tanh_c[k]);
+#pragma unroll
+                        for (int c = 0; c < kKeys; c += 2) {
+                            const uint64_t x = f2(sc[c], sc[c + 1]), v = f2_mul(x, x);
+                            uint64_t y = f2_fma(tc[4], v, tc[3]);
+                            y = f2_fma(y, v, tc[2]);
+                            y = f2_fma(y, v, tc[1]);
+                            y = f2_fma(y, v, tc[0]);
+                            f2_split(f2_mul(x, y), sc[c], sc[c + 1]);
+                        }
+                    } else {
+                        // z = cap' tanh(x) = cap' - 2 cap' / (1 + e^2x)
+                        const float k2 = 2.f * kScoreLog2e * md.cap_in;
+#pragma unroll
+                        for (int c = 0; c < kKeys; ++c)
+                            sc[c] = fmaf(-2.f * md.cap_out, fast_rcp(1.f + fast_exp2(k2 * sc[c])),
+                                         md.cap_out);
+                        mul = 1.f;
+                    }
+                }
+                if constexpr (kBias) {
+                    // distance |p - t|: keys before the row's position for all but
+                    // the tiles at the diagonal or in a prefix
+                    if (__all_sync(0xffffffffu, key0 + kKeys - 1 <= pos)) {
+                        const float base = slope2 * (float)(key0 - pos);
+#pragma unroll
+                        for (int c = 0; c < kKeys; c += 2) {
+                            const uint64_t bb = f2(fmaf(slope2, (float)c, base),
+                                                   fmaf(slope2, (float)(c + 1), base));
+                            f2_split(f2_fma(f2(sc[c], sc[c + 1]), f2(mul, mul), bb), sc[c],
+                                     sc[c + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kKeys; ++c)
+                            sc[c] = fmaf(-slope2, fabsf((float)(key0 + c - pos)), sc[c] * mul);
+                    }
+                    mul = 1.f;
+                } else if (mul <= 0.f) {  // a maximum of z / mul needs mul > 0
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c) sc[c] *= mul;
+                    mul = 1.f;
+                }
+                if (!whole) {  // select: hidden scores may be anything
+                    const int a = lo - key0, e = hi - key0;  // visible: a <= c < e
+#pragma unroll
+                    for (int w = 0; w < kKeys / 32; ++w) {
+                        const int f0 = min(max(a - 32 * w, 0), 32), f1 = min(max(e - 32 * w, 0), 32);
+                        uint32_t see = (f1 == 32 ? 0xffffffffu : (1u << f1) - 1u) &
+                                       (f0 == 32 ? 0u : 0xffffffffu << f0);
+                        if ((bad >> (2 * w)) & 1u) see &= 0xffff0000u;
+                        if ((bad >> (2 * w + 1)) & 1u) see &= 0x0000ffffu;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            sc[32 * w + c] = (see >> c) & 1u ? sc[32 * w + c] : -INFINITY;
+                    }
+                }
+                float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 2)
+                    mxp[(c >> 1) & 3] = max3(mxp[(c >> 1) & 3], sc[c], sc[c + 1]);
+                const float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mul;
+                const float m_new = fmaxf(m_used, mx);
+                // lazy rescale: only when the maximum grew by more than 2^kRescale
+                const bool grow = m_used != -INFINITY && m_new > m_used + kRescale;
+                const float f = grow ? fast_exp2(m_used - m_new) : 1.f;
+                if (m_used == -INFINITY || grow) m_used = m_new;
+                const float ms = m_used == -INFINITY ? 0.f : m_used;
+                if (__any_sync(0xffffffffu, grow)) {
+                    // S_X(J) was issued after P V_X(J-1): O_X holds every earlier tile
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tc_ld32(ox + 32 * c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc_st32(ox + 32 * c, o);
+                    }
+                }
+                // P as 16-bit pairs over the first 64 columns (every score is in
+                // registers); the sum takes the unrounded weights
+                const uint64_t mul2 = f2(mul, mul), nms2 = f2(-ms, -ms);
+                uint64_t acc2[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+                for (int c4 = 0; c4 < kKeys / 32; ++c4) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float a0, a1;
+                        f2_split(f2_fma(f2(sc[32 * c4 + 2 * e], sc[32 * c4 + 2 * e + 1]), mul2,
+                                        nms2),
+                                 a0, a1);
+                        const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                        acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
+                        pk[e] = E::pack(p0, p1);
+                    }
+                    tc_st16(sx + 16 * c4, pk);
+                }
+                float psp[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f2_split(acc2[e], psp[2 * e], psp[2 * e + 1]);
+                const float psum = ((psp[0] + psp[1]) + (psp[2] + psp[3])) +
+                                   ((psp[4] + psp[5]) + (psp[6] + psp[7]));
+                tc_wait_st();
+                l = l * f + psum;
+                // V rows that no row of the item sees (or that were not loaded)
+                // become zeros before P V; both tiles zero the same rows
+                if (j == 0 || j == it.nkv - 1 || bad) {
+                    unsigned char* vt = sv + b * TILE;
+                    for (int x = r; x < kKeys * 8 * HALVES; x += kRows) {
+                        const int kq = x / (8 * HALVES), rest = x - kq * (8 * HALVES);
+                        const int key = key0 + kq;
+                        if (key >= it.lo && key < it.hi && !((bad >> (kq >> 4)) & 1u)) continue;
+                        *reinterpret_cast<uint4*>(vt + (rest >> 3) * REG + kq * 128 +
+                                                  ((rest & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                tc_fence_before();  // P and a rescaled O are ordered before the next MMA
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[X]);
+            }
+            if (!ok) break;
+            // ---- epilogue: O_X / l for the rows of the chunk, or their partials
+            const bool split = p.splits > 1;
+            T* dst = static_cast<T*>(p.out) +
+                     ((size_t)(it.q0 + (live_row ? t : 0)) * Hq + head) * D;
+            const size_t prow =
+                ((size_t)it.base * p.splits + it.split) * kPair + X * kRows + r;
+            if (split && live_row) {
+                p.ws_m[prow] = m_used;
+                p.ws_l[prow] = l;
+            }
+            if (it.nkv == 0) {  // nothing visible: zeros (a split's joiner skips it: l = 0)
+                if (live_row && !split)
+                    for (int c = 0; c < D / 8; ++c)
+                        *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_ready[X], items & 1, abort_flag, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            bool finite = true;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tc_ld32(ox + 32 * c, o);
+                tc_wait_ld();
+                float sum = 0.f;  // finite values times zero: NaN if one is not finite
+#pragma unroll
+                for (int e = 0; e < 32; ++e) sum = fmaf(0.f, __uint_as_float(o[e]), sum);
+                finite = finite && sum == 0.f;
+                if (!live_row) continue;
+                if (split) {
+                    float* od = p.ws_o + prow * D + 32 * c;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w8[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) w8[u] = o[8 * e + u];
+                        st_global_v8(od + 8 * e, w8);
+                    }
+                    continue;
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    w[u] = l != 0.f ? E::pack(__uint_as_float(o[2 * u]) * inv,
+                                              __uint_as_float(o[2 * u + 1]) * inv)
+                                    : 0u;
+                if (out32) {
+                    // 32-byte stores: each fills a whole L2 sector
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t w8[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) w8[u] = w[8 * hh + u];
+                        st_global_v8(dst + 32 * c + 16 * hh, w8);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(dst + 32 * c + 8 * e) =
+                            make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[X]);
+            ++items;
+            // rows that met something not finite: again, from their own keys
+            unsigned redo = __ballot_sync(0xffffffffu, live_row && l != 0.f && !finite);
+            while (redo) {
+                const int who = __ffs(redo) - 1;
+                redo &= redo - 1;
+                const int R2 = it.row0 + X * kRows + 32 * wq + who, t2 = R2 / g;
+                const int pos2 = it.n - it.qlen + t2, head2 = it.h * g + R2 - t2 * g;
+                const int klo = max(first_key(md, it.s, pos2), it.b0 * PKV_BLOCK_SIZE);
+                const int khi = min(end_key(md, it.s, pos2, it.n),
+                                    (it.b0 + it.nblk) * PKV_BLOCK_SIZE);
+                float o[D / 32], m2, l2;
+                plain_row<T, D>(p, it.s, it.h, head2, it.q0 + t2, pos2, klo, khi, o, m2, l2);
+                const size_t prow2 = prow - lane + who;
+                T* dst2 = static_cast<T*>(p.out) + ((size_t)(it.q0 + t2) * Hq + head2) * D;
+                const float inv2 = l2 != 0.f ? 1.f / l2 : 0.f;
+#pragma unroll
+                for (int e = 0; e < D / 32; e += 2) {
+                    const int d = lane * (D / 32) + e;
+                    if (split) {
+                        p.ws_o[prow2 * D + d] = o[e];
+                        p.ws_o[prow2 * D + d + 1] = o[e + 1];
+                    } else {
+                        *reinterpret_cast<uint32_t*>(dst2 + d) =
+                            E::pack(o[e] * inv2, o[e + 1] * inv2);
+                    }
+                }
+                if (split && lane == 0) {
+                    p.ws_m[prow2] = m2;
+                    p.ws_l[prow2] = l2;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tc_dealloc(tmem, kCols);
+    }
+}
+
+// Joins the splits of one item's rows, a warp per row:
+//   M = max m,  out = sum o 2^(m - M) / sum l 2^(m - M).
+constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 32;  // rows of an item per CTA
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) scored_prefill_join_kernel(const PrefillScored p) {
+    constexpr int PER = D / 32;
+    const int base = blockIdx.x / (kPair / kJoinRows);
+    const int pair = base % p.pairs_per_seq;
+    const int h = base / p.pairs_per_seq % p.num_kv_heads;
+    const int s = base / p.pairs_per_seq / p.num_kv_heads;
+    const int q0 = p.cu_q_lens[s], qlen = p.cu_q_lens[s + 1] - q0, n = p.context_lens[s];
+    if (!lengths_ok(p, q0, qlen, n)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = p.group, S = p.splits;
+    const int r0 = blockIdx.x % (kPair / kJoinRows) * kJoinRows;
+    for (int r = r0 + warp; r < r0 + kJoinRows; r += kJoinWarps) {
+        const int R = pair * kPair + r;
+        if (R >= qlen * g) return;
+        const int t = R / g, head = h * g + R - t * g;
+        const size_t row = (size_t)base * S * kPair + r;
+        float M = -INFINITY;
+        for (int k = 0; k < S; ++k) M = fmaxf(M, p.ws_m[row + (size_t)k * kPair]);
+        if (M == -INFINITY) M = 0.f;
+        float L = 0.f, acc[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+        for (int k = 0; k < S; ++k) {
+            const size_t kr = row + (size_t)k * kPair;
+            const float lk = p.ws_l[kr];
+            if (lk == 0.f) continue;  // a split without visible keys wrote no o
+            const float w = fast_exp2(p.ws_m[kr] - M);
+            L += w * lk;
+            const float* o = p.ws_o + kr * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, o[e], acc[e]);
+        }
+        const float inv = L != 0.f ? 1.f / L : 0.f;
+        T* dst = static_cast<T*>(p.out) + ((size_t)(q0 + t) * p.num_q_heads + head) * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; e += 2)
+            *reinterpret_cast<uint32_t*>(dst + e) = Elem<T>::pack(acc[e] * inv, acc[e + 1] * inv);
+    }
+}
+
+// Items before splitting, and into how many key runs each is cut: enough for
+// every SM, but none shorter than two key tiles.
+struct Plan {
+    long long items;
+    int pairs, splits;
+};
+
+Plan make_plan(int num_seqs, int max_q_len, int num_kv_heads, int group, int ctas,
+               long long max_tiles) {
+    Plan pl;
+    pl.pairs = (int)(((long long)max_q_len * group + kPair - 1) / kPair);
+    pl.items = (long long)num_seqs * num_kv_heads * pl.pairs;
+    const long long by_ctas = pl.items > 0 ? ctas / pl.items : 1;
+    pl.splits = (int)std::max<long long>(1, std::min(by_ctas, max_tiles / 2));
+    return pl;
+}
+
+struct Workspace {
+    size_t m, l, o, total;
+};
+
+Workspace ws_layout(long long rows, int head_dim) {
+    Workspace w;
+    w.m = 0;
+    w.l = align256((size_t)rows * 4);
+    w.o = w.l + align256((size_t)rows * 4);
+    w.total = w.o + (size_t)rows * head_dim * 4;
+    return w;
+}
+
+template <int D>
+size_t prefill_smem() {
+    // 2 Q tiles, 2 K and 2 V stages, barriers (under 1 KB); 1 KB alignment slack
+    return 1024 + (size_t)6 * (D / 64) * kRows * 128 + 1024;
+}
+
+template <typename T, int D, bool kCap, bool kBias>
+pkv_status launch(const PrefillScored& prm, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                  const CUtensorMap& tmq, int q_tma, int items, int ctas, cudaStream_t stream) {
+    auto kern = scored_prefill_kernel<T, D, kCap, kBias>;
+    // the register shares assume the launch count of this build
+    static const bool regs_ok = [&] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == kLaunchRegs;
+    }();
+    if (!regs_ok) return PKV_ERR_CUDA;
+    const size_t smem = prefill_smem<D>();
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess)
+        return PKV_ERR_CUDA;
+    kern<<<std::min(items, ctas), kThreads, smem, stream>>>(prm, tmk, tmv, tmq, q_tma, items);
+    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+    if (prm.splits == 1) return PKV_OK;
+    scored_prefill_join_kernel<T, D>
+        <<<items / prm.splits * (kPair / kJoinRows), kJoinWarps * 32, 0, stream>>>(prm);
+    return cuda_status(cudaGetLastError());
+}
+
+template <typename T, int D>
+pkv_status launch_mods(const PrefillScored& prm, pkv_dtype dtype, int items, int ctas,
+                       cudaStream_t stream) {
+    CUtensorMap tmk, tmv, tmq;
+    if (!make_pool_map(&tmk, prm.k_cache, prm.num_blocks, prm.num_kv_heads, D, dtype) ||
+        !make_pool_map(&tmv, prm.v_cache, prm.num_blocks, prm.num_kv_heads, D, dtype))
+        return PKV_ERR_CUDA;
+    const int q_tma =
+        make_q_tile_map(&tmq, prm.q, prm.num_q_rows, prm.num_q_heads, D, prm.group, dtype) ? 1 : 0;
+    if (!q_tma) tmq = tmk;  // unused
+    const bool cap = prm.mods.cap_out > 0.f, bias = prm.mods.slopes != nullptr;
+    if (cap)
+        return bias ? launch<T, D, true, true>(prm, tmk, tmv, tmq, q_tma, items, ctas, stream)
+                    : launch<T, D, true, false>(prm, tmk, tmv, tmq, q_tma, items, ctas, stream);
+    return bias ? launch<T, D, false, true>(prm, tmk, tmv, tmq, q_tma, items, ctas, stream)
+                : launch<T, D, false, false>(prm, tmk, tmv, tmq, q_tma, items, ctas, stream);
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+size_t paged_attention_prefill_scored_workspace_bytes(int num_seqs, int max_q_len, int num_q_heads,
+                                                      int num_kv_heads, int head_dim) {
+    if (num_seqs <= 0 || max_q_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        num_q_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+        return 0;
+    const pkv::Plan pl = pkv::make_plan(num_seqs, max_q_len, num_kv_heads,
+                                        num_q_heads / num_kv_heads, pkv::kMaxCtas, 1 << 30);
+    if (pl.splits == 1) return 256;
+    return pkv::ws_layout(pl.items * pl.splits * pkv::kPair, head_dim).total;
+}
+
+pkv_status paged_attention_prefill_scored(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* context_lens, const int32_t* cu_q_lens, int num_seqs,
+    int max_q_len, int num_q_rows, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+    float scale, float softcap, const float* alibi_slopes, int window, const int32_t* key_starts,
+    const int32_t* prefix_lens, void* out, void* workspace, size_t workspace_bytes,
+    pkv_dtype dtype, pkv_stream_t stream) {
+    if (num_seqs < 0 || max_q_len < 0 || num_q_rows < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        head_dim <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (num_q_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+    if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+    pkv::PrefillScored prm = {};
+    if (!pkv::make_score_mods(&prm.mods, scale, softcap, alibi_slopes, window, key_starts,
+                              prefix_lens))
+        return PKV_ERR_INVALID_ARG;
+    const int g = num_q_heads / num_kv_heads;
+    if (g > pkv::kMaxGroup || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
+    if (max_blocks_per_seq > 0x7fffffff / PKV_BLOCK_SIZE ||
+        num_blocks > 0x7fffffff / PKV_BLOCK_SIZE || max_q_len > 0x7fffffff / 32 - 256)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_q_len == 0 || num_q_rows == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_q_lens || !out)
+        return PKV_ERR_INVALID_ARG;
+    if (!pkv::aligned16(q) || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache) ||
+        !pkv::aligned16(out))
+        return PKV_ERR_INVALID_ARG;
+    const size_t need = paged_attention_prefill_scored_workspace_bytes(
+        num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PKV_ERR_WORKSPACE;
+    prm.status = pkv::status_word();
+    const int sms = pkv::sm_count();
+    if (!prm.status || sms <= 0) return PKV_ERR_CUDA;
+    const int ctas = std::min(sms, pkv::kMaxCtas);
+    // most key tiles of an item
+    long long keys = (long long)max_blocks_per_seq * PKV_BLOCK_SIZE;
+    if (window > 0) keys = std::min(keys, (long long)window + max_q_len + PKV_BLOCK_SIZE);
+    const pkv::Plan pl = pkv::make_plan(num_seqs, max_q_len, num_kv_heads, g, ctas,
+                                        (keys + pkv::kKeys - 1) / pkv::kKeys);
+    if (pl.items * pl.splits > 0x7fffffffll / 64) return PKV_ERR_UNSUPPORTED;
+    prm.q = q;
+    prm.k_cache = k_cache;
+    prm.v_cache = v_cache;
+    prm.out = out;
+    prm.block_tables = block_tables;
+    prm.context_lens = context_lens;
+    prm.cu_q_lens = cu_q_lens;
+    prm.num_seqs = num_seqs;
+    prm.num_q_heads = num_q_heads;
+    prm.num_kv_heads = num_kv_heads;
+    prm.group = g;
+    prm.max_blocks_per_seq = max_blocks_per_seq;
+    prm.num_blocks = num_blocks;
+    prm.max_q_len = max_q_len;
+    prm.num_q_rows = num_q_rows;
+    prm.pairs_per_seq = pl.pairs;
+    prm.splits = pl.splits;
+    // the polynomial's terms for raw scores: tanh(x) / x = sum c_i x^2i, x = raw cap_in
+    prm.tanh_limit = -1.f;
+    if (softcap > 0.f && scale != 0.f) {
+        const double c2 = (double)prm.mods.cap_in * prm.mods.cap_in;
+        double f = 1.0;
+        bool ok = true;
+        for (int i = 0; i < pkv::kTanhTerms; ++i, f *= c2) {
+            prm.tanh_c[i] = (float)(pkv::tanh_term(i) * f);
+            ok = ok && std::isnormal(prm.tanh_c[i]);
+        }
+        const float limit = pkv::kTanhRange / std::fabs(prm.mods.cap_in);
+        // raw^2 must stay finite too
+        if (ok && limit < 1e18f) prm.tanh_limit = limit;
+    }
+    const pkv::Workspace ws =
+        pkv::ws_layout(pl.splits > 1 ? pl.items * pl.splits * pkv::kPair : 0, head_dim);
+    char* w = static_cast<char*>(workspace);
+    prm.ws_m = reinterpret_cast<float*>(w + ws.m);
+    prm.ws_l = reinterpret_cast<float*>(w + ws.l);
+    prm.ws_o = reinterpret_cast<float*>(w + ws.o);
+    const int items = (int)(pl.items * pl.splits);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == PKV_BF16)
+        return head_dim == 128
+                   ? pkv::launch_mods<__nv_bfloat16, 128>(prm, dtype, items, ctas, st)
+                   : pkv::launch_mods<__nv_bfloat16, 64>(prm, dtype, items, ctas, st);
+    return head_dim == 128 ? pkv::launch_mods<__half, 128>(prm, dtype, items, ctas, st)
+                           : pkv::launch_mods<__half, 64>(prm, dtype, items, ctas, st);
+}
+
+}  // extern "C"
