@@ -553,27 +553,53 @@ def paged_kv_rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1
     return inv_freq.to(device), rope_scale.value
 
 
-def _one_device(**tensors):
-    """All given tensors on the current CUDA device (the kernels launch there)."""
-    for name, t in tensors.items():
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.device("cuda", torch.cuda.current_device())
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on the current device {dev}")
+def _pointers(*named):
+    """Device pointers of (name, contiguous tensor or None) pairs, all on the current
+    CUDA device (where the kernels launch)."""
+    dev = named[0][1].get_device()
+    ptrs = []
+    for name, t in named:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.get_device() != dev or dev < 0:
+            _refuse_device(name, t)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous (pass a view of one layer's pool)")
+        ptrs.append(t.data_ptr())
+    if dev != torch.cuda.current_device():
+        _refuse_device(*named[0])
+    return ptrs
 
 
-def _rows(t: torch.Tensor, name: str):
+def _refuse_device(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} is on {t.device}; every tensor must be on the current device, "
+                     f"cuda:{torch.cuda.current_device()}")
+
+
+def _stream_handle(stream):
+    """_stream, without making a Stream object for the current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _stream(stream)
+
+
+def _rows(name: str, t: torch.Tensor, dev: int):
     """Pointer and token stride of rows [T, heads, D] whose heads are packed (the
     tokens may be spaced, as in a view of a wider projection's rows)."""
+    if t.get_device() != dev or dev < 0:
+        _refuse_device(name, t)
     T, H, D = t.shape
-    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name} must have contiguous heads (only the token stride is free)")
-    stride = t.stride(0) if T > 1 else -(-H * D // 8) * 8
-    if stride < H * D:
+    if T <= 1:
+        st = -(-H * D // 8) * 8
+    elif st < H * D:
         raise ValueError(f"{name}'s tokens must not overlap")
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), st
 
 
 def _check_rope(q, k_new, v_new, k_cache, v_cache, inv_freq, q_out):
@@ -599,14 +625,16 @@ def paged_kv_rope_write(q, k_new, v_new, k_cache, v_cache, positions, slot_mappi
         raise ValueError("positions must be int32 [num_tokens]")
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be int64 [num_tokens]")
-    _one_device(q=q, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
-                positions=positions, slot_mapping=slot_mapping, inv_freq=inv_freq, q_out=q_out)
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k_new, "k_new"), _rows(v_new, "v_new")
+    dev = q_out.get_device()
+    (qp, qs), (kp, ks) = _rows("q", q, dev), _rows("k_new", k_new, dev)
+    vp, vs = _rows("v_new", v_new, dev)
+    out, kc, vc, pos, slots, freq = _pointers(
+        ("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache), ("positions", positions),
+        ("slot_mapping", slot_mapping), ("inv_freq", inv_freq))
     _check("paged_kv_rope_write", lib().paged_kv_rope_write(
-        qp, kp, vp, qs, ks, vs, _dev(positions, "positions"), _dev(slot_mapping, "slot_mapping"),
-        _dev(inv_freq, "inv_freq"), float(rope_scale), T, Hq, Hkv, D, 2 * inv_freq.numel(),
-        int(bool(interleaved)), NB, _dev(q_out, "q_out"), _dev(k_cache, "k_cache"),
-        _dev(v_cache, "v_cache"), _dtype_code(q), _stream(stream)))
+        qp, kp, vp, qs, ks, vs, pos, slots, freq, float(rope_scale), T, Hq, Hkv, D,
+        2 * inv_freq.shape[0], 1 if interleaved else 0, NB, out, kc, vc, _dtype_code(q),
+        _stream_handle(stream)))
     return q_out
 
 
@@ -617,16 +645,17 @@ def paged_kv_rope_write_new_tokens(q, k_new, v_new, k_cache, v_cache, block_tabl
     B, Hq, Hkv, D, NB = _check_rope(q, k_new, v_new, k_cache, v_cache, inv_freq, q_out)
     _check_tables(block_tables, context_lens, B)
     _check_slots(slot_mapping_out, B, "slot_mapping_out")
-    _one_device(q=q, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
-                block_tables=block_tables, context_lens=context_lens, inv_freq=inv_freq,
-                q_out=q_out, slot_mapping_out=slot_mapping_out)
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k_new, "k_new"), _rows(v_new, "v_new")
+    dev = q_out.get_device()
+    (qp, qs), (kp, ks) = _rows("q", q, dev), _rows("k_new", k_new, dev)
+    vp, vs = _rows("v_new", v_new, dev)
+    out, kc, vc, bt, cl, freq, slots = _pointers(
+        ("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache),
+        ("block_tables", block_tables), ("context_lens", context_lens), ("inv_freq", inv_freq),
+        ("slot_mapping_out", slot_mapping_out))
     _check("paged_kv_rope_write_new_tokens", lib().paged_kv_rope_write_new_tokens(
-        qp, kp, vp, qs, ks, vs, _dev(block_tables, "block_tables"), block_tables.shape[1],
-        _dev(context_lens, "context_lens"), _dev(inv_freq, "inv_freq"), float(rope_scale), B, Hq,
-        Hkv, D, 2 * inv_freq.numel(), int(bool(interleaved)), NB, _dev(q_out, "q_out"),
-        _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-        _opt(slot_mapping_out, "slot_mapping_out"), _dtype_code(q), _stream(stream)))
+        qp, kp, vp, qs, ks, vs, bt, block_tables.shape[1], cl, freq, float(rope_scale), B, Hq, Hkv, D,
+        2 * inv_freq.shape[0], 1 if interleaved else 0, NB, out, kc, vc, slots, _dtype_code(q),
+        _stream_handle(stream)))
     return q_out
 
 
@@ -642,6 +671,13 @@ def new_scored_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, max_cont
     n = paged_attention_decode_scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads,
                                                       head_dim, max_context_len)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _int32(value, name) -> int:
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:  # ctypes would cut it to its low 32 bits
+        raise ValueError(f"{name} must fit 32 bits")
+    return value
 
 
 def _check_score_mods(Hq, B, alibi_slopes, **per_seq):
@@ -662,16 +698,15 @@ def paged_attention_decode_scored(q, k_cache, v_cache, block_tables, context_len
     B, Hq, Hkv, D, NB = _check_decode_shapes(q, k_cache, v_cache, block_tables, context_lens,
                                              out)
     _check_score_mods(Hq, B, alibi_slopes, key_starts=key_starts)
-    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                context_lens=context_lens, out=out, workspace=workspace,
-                alibi_slopes=alibi_slopes, key_starts=key_starts)
+    qp, kc, vc, bt, cl, op, ws, slopes, starts = _pointers(
+        ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
+        ("context_lens", context_lens), ("out", out), ("workspace", workspace),
+        ("alibi_slopes", alibi_slopes), ("key_starts", key_starts))
     _check("paged_attention_decode_scored", lib().paged_attention_decode_scored(
-        _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-        _dev(block_tables, "block_tables"), block_tables.shape[1],
-        _dev(context_lens, "context_lens"), int(max_context_len), B, Hq, Hkv, D, NB,
-        float(scale), float(softcap), _opt(alibi_slopes, "alibi_slopes"), int(window),
-        _opt(key_starts, "key_starts"), _dev(out, "out"), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream)))
+        qp, kc, vc, bt, block_tables.shape[1], cl, _int32(max_context_len, "max_context_len"), B,
+        Hq, Hkv, D, NB, float(scale), float(softcap), slopes, _int32(window, "window"), starts,
+        op, ws, workspace.numel() * workspace.element_size(), _dtype_code(q),
+        _stream_handle(stream)))
     return out
 
 
@@ -705,17 +740,16 @@ def paged_attention_prefill_scored(q, k_cache, v_cache, block_tables, context_le
         raise ValueError("cu_q_lens must be int32 [num_seqs + 1]")
     _check_dtypes(q, k_cache, v_cache, out)
     _check_score_mods(Hq, B, alibi_slopes, key_starts=key_starts, prefix_lens=prefix_lens)
-    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                context_lens=context_lens, cu_q_lens=cu_q_lens, out=out, workspace=workspace,
-                alibi_slopes=alibi_slopes, key_starts=key_starts, prefix_lens=prefix_lens)
+    qp, kc, vc, bt, cl, cu, op, ws, slopes, starts, prefixes = _pointers(
+        ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
+        ("context_lens", context_lens), ("cu_q_lens", cu_q_lens), ("out", out),
+        ("workspace", workspace), ("alibi_slopes", alibi_slopes), ("key_starts", key_starts),
+        ("prefix_lens", prefix_lens))
     _check("paged_attention_prefill_scored", lib().paged_attention_prefill_scored(
-        _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-        _dev(block_tables, "block_tables"), block_tables.shape[1],
-        _dev(context_lens, "context_lens"), _dev(cu_q_lens, "cu_q_lens"), B, int(max_q_len), R,
-        Hq, Hkv, D, NB, float(scale), float(softcap), _opt(alibi_slopes, "alibi_slopes"),
-        int(window), _opt(key_starts, "key_starts"), _opt(prefix_lens, "prefix_lens"),
-        _dev(out, "out"), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _dtype_code(q), _stream(stream)))
+        qp, kc, vc, bt, block_tables.shape[1], cl, cu, B, _int32(max_q_len, "max_q_len"), R, Hq,
+        Hkv, D, NB, float(scale), float(softcap), slopes, _int32(window, "window"), starts,
+        prefixes, op, ws,
+        workspace.numel() * workspace.element_size(), _dtype_code(q), _stream_handle(stream)))
     return out
 
 

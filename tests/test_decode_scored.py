@@ -35,7 +35,7 @@ def _cpu_args(**over):
     (dict(key_starts=torch.zeros(4, dtype=torch.int32)), "key_starts must be int32"),
     (dict(context_lens=torch.ones(2, dtype=torch.int32)), "context_lens must be int32"),
     (dict(out=torch.zeros(3, 8, 64, dtype=f16)), "share one dtype"),
-    (dict(), "must be a CUDA tensor"),
+    (dict(), "must be a CUDA tensor"),  # (the refusal that every well-formed call here meets)
 ])
 def test_decode_scored_refuses(over, msg):
     with pytest.raises(ValueError, match=msg):

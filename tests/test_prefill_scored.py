@@ -36,7 +36,7 @@ def _cpu_args(**over):
     (dict(cu_q_lens=torch.zeros(2, dtype=torch.int32)), "cu_q_lens must be int32"),
     (dict(out=torch.zeros(5, 8, 64, dtype=f16)), "share one dtype"),
     (dict(v_cache=torch.zeros(10, 16, 2, 32, dtype=bf)), "pool shape"),
-    (dict(), "must be a CUDA tensor"),
+    (dict(), "must be a CUDA tensor"),  # (the refusal that every well-formed call here meets)
 ])
 def test_prefill_scored_refuses(over, msg):
     with pytest.raises(ValueError, match=msg):
