@@ -37,20 +37,23 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kSoftWarps = 16;         // score warps: tile A / B x key half x lane quarter
+constexpr int kThreads = (4 + kSoftWarps) * 32;
 constexpr int kRows = 128;             // rows of a tile
 constexpr int kPair = 2 * kRows;       // rows of an item
 constexpr int kKeys = 128;             // keys of a key tile
+constexpr int kHalf = kKeys / 2;       // keys of one score thread
 constexpr int kTileBlocks = kKeys / PKV_BLOCK_SIZE;
 constexpr float kRescale = 8.f;        // log2 of the largest P before O is rescaled
+constexpr float kFixedMax = 80.f;      // largest |z| (base 2) that needs no running maximum
 constexpr int kMaxCtas = 160;          // bounds the workspace of split items
 constexpr int kMaxGroup = 16;
 // Registers: launched at kLaunchRegs a thread (checked on the host); the load /
-// MMA warpgroup gives some up and the two softmax warpgroups take them.
-constexpr int kLaunchRegs = 168;
-constexpr int kOtherRegs = 88;
-constexpr int kSoftmaxRegs = 208;
-static_assert(128 * kOtherRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs,
+// MMA warpgroup gives some up and the four score warpgroups take them.
+constexpr int kLaunchRegs = 96;
+constexpr int kOtherRegs = 56;
+constexpr int kSoftmaxRegs = 104;
+static_assert(128 * kOtherRegs + kSoftWarps * 32 * kSoftmaxRegs <= kThreads * kLaunchRegs,
               "register shares exceed the launch total");
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -77,8 +80,8 @@ struct PrefillScored {
     int max_q_len, num_q_rows;
     int pairs_per_seq;     // ceil(max_q_len * group / kPair)
     int splits;            // key runs per item; > 1: partials go to the workspace
-    float tanh_c[kTanhTerms];  // the polynomial's terms in (raw score)^2
-    float tanh_limit;      // largest |raw score| it serves (negative: none)
+    float tanh_z[kTanhTerms];  // the polynomial's terms: z = raw sum tanh_z[i] raw^2i
+    float tanh_limit;      // largest (raw score)^2 it serves (negative: none)
     // partials of split items: row = ((base item) * splits + split) * kPair + row of the pair
     float* ws_m;
     float* ws_l;
@@ -256,7 +259,51 @@ __device__ __noinline__ void plain_row(const PrefillScored& p, int s, int h, int
     }
 }
 
-template <typename T, int D, bool kCap, bool kBias>
+// 32 raw scores to capped base-2 scores z = cap' tanh(raw cap_in), cap' = cap
+// log2(e).  Where the whole warp's scores allow it z is raw times a polynomial
+// in raw^2, two scores an instruction; else cap' - 2 cap' / (1 + e^2x).
+__device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[32]) {
+    uint64_t v[16];
+    float top[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const uint64_t x = f2(sc[2 * e], sc[2 * e + 1]);
+        v[e] = f2_mul(x, x);
+        float a0, a1;
+        f2_split(v[e], a0, a1);
+        top[e & 1] = max3(top[e & 1], a0, a1);
+    }
+    if (__all_sync(0xffffffffu, fmaxf(top[0], top[1]) <= p.tanh_limit)) {
+        const uint64_t c4 = f2(p.tanh_z[4], p.tanh_z[4]), c3 = f2(p.tanh_z[3], p.tanh_z[3]);
+        const uint64_t c2 = f2(p.tanh_z[2], p.tanh_z[2]), c1 = f2(p.tanh_z[1], p.tanh_z[1]);
+        const uint64_t c0 = f2(p.tanh_z[0], p.tanh_z[0]);
+#pragma unroll
+        for (int e0 = 0; e0 < 16; e0 += 4) {  // four independent chains at a time
+            uint64_t y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = f2_fma(c4, v[e0 + u], c3);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[e0 + u], c2);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[e0 + u], c1);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[e0 + u], c0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int e = e0 + u;
+                f2_split(f2_mul(f2(sc[2 * e], sc[2 * e + 1]), y[u]), sc[2 * e], sc[2 * e + 1]);
+            }
+        }
+    } else {
+        const float k2 = 2.f * kScoreLog2e * p.mods.cap_in;
+        const float cap = p.mods.cap_out;
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            sc[c] = fmaf(-2.f * cap, fast_rcp(1.f + fast_exp2(k2 * sc[c])), cap);
+    }
+}
+
+template <typename T, int D, bool kCap, bool kBias, bool kFixed>
 __global__ void __launch_bounds__(kThreads, 1)
     scored_prefill_kernel(const PrefillScored p, const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_v,
@@ -280,13 +327,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* q_full = bars + 8;            // [tile]
     uint64_t* q_empty = bars + 10;
     uint64_t* s_full = bars + 12;           // [tile]: S_X written
-    uint64_t* p_full = bars + 14;           // [tile]: its 4 softmax warps wrote P_X
-    uint64_t* o_ready = bars + 16;          // [tile]: an item's last P V_X done
-    uint64_t* o_free = bars + 18;           // [tile]: its softmax warps read O_X
-    uint64_t* mma_idle = bars + 20;
-    int* vbad = reinterpret_cast<int*>(bars + 21);           // [2] bad-block bits per V stage
+    uint64_t* p_full = bars + 14;           // [tile][key half]: its 4 warps wrote P
+    uint64_t* o_ready = bars + 18;          // [tile]: an item's last P V_X done
+    uint64_t* o_free = bars + 20;           // [tile]: its score warps read O_X
+    uint64_t* mma_idle = bars + 22;
+    uint64_t* x_max = bars + 23;            // [tile][lane quarter]: both halves' maxima written
+    uint64_t* x_sum = bars + 31;            // [tile][lane quarter]: both halves' sums written
+    int* vbad = reinterpret_cast<int*>(bars + 39);           // [2] bad-block bits per V stage
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vbad + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    // what the two key halves of a row tell each other, by parity:
+    // [parity][tile][half][row] maxima, and sums (NaN: O is not finite)
+    float* xm = reinterpret_cast<float*>(tmem_slot + 2);
+    float* xl = xm + 2 * 2 * 2 * kRows;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = p.group, Hq = p.num_q_heads;
@@ -300,9 +353,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_ready[i], 1);
-            mbar_init(&o_free[i], 4);
+            mbar_init(&o_free[i], 8);
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&x_max[i], 2);
+            mbar_init(&x_sum[i], 2);
         }
         mbar_init(mma_idle, 1);
         *abort_flag = 0;
@@ -474,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c.j == c.nkv - 1) tc_commit(&q_empty[X]);
                 return true;
             };
-            // O_X += P_X(c) V(c): P_X over the first 64 columns of its scores
+            // O_X += P_X(c) V(c): the P of a key half over the first 32 columns
+            // of that half's scores
             auto issue_pv = [&](const Cur& c, int X) -> bool {
                 const int b = c.J & 1;
                 if (X == 0 && !mbar_wait(&v_full[b], (c.J >> 1) & 1, abort_flag, p.status))
@@ -483,13 +542,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c.j == 0 && c.items[X] >= 1 &&
                     !mbar_wait(&o_free[X], (c.items[X] - 1) & 1, abort_flag, p.status))
                     return false;
-                if (!mbar_wait(&p_full[X], c.tiles[X] & 1, abort_flag, p.status)) return false;
-                tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    tc_mma_tmem_a(tmem + kOCol + X * D, tmem + X * kKeys + 8 * kk,
-                                  tc_smem_desc(av + b * TILE + kk * 2048, REG, 1024), id_pv,
-                                  c.j > 0 || kk > 0);
+                for (int q = 0; q < 2; ++q) {
+                    if (!mbar_wait(&p_full[2 * X + q], c.tiles[X] & 1, abort_flag, p.status))
+                        return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kHalf / 16; ++kk)
+                        tc_mma_tmem_a(tmem + kOCol + X * D, tmem + X * kKeys + kHalf * q + 8 * kk,
+                                      tc_smem_desc(av + b * TILE + (q * (kHalf / 16) + kk) * 2048,
+                                                   REG, 1024),
+                                      id_pv, c.j > 0 || q > 0 || kk > 0);
+                }
                 if (X == 1 || !c.has_b) tc_commit(&v_empty[b]);
                 if (c.j == c.nkv - 1) tc_commit(&o_ready[X]);
                 return true;
@@ -513,16 +577,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
-        // ---------------- scores of tile X (warps 4-7: A, 8-11: B), one thread per row
-        const int X = (warp - 4) >> 2;
+        // ---------- scores of tile X, keys 64 q .. of each key tile: warps 4-7 A
+        // first half, 8-11 A second, 12-15 and 16-19 B; one thread per row and half
+        const int X = (warp - 4) >> 3, q = ((warp - 4) >> 2) & 1;
         const int wq = warp & 3;                             // tensor-memory lane quarter
         const int r = 32 * wq + lane;                        // row of the tile
         const uint32_t trow = tmem + ((uint32_t)(32 * wq) << 16);
-        const uint32_t sx = trow + X * kKeys;                // this tile's scores / P
-        const uint32_t ox = trow + kOCol + X * D;            // this tile's O
+        const uint32_t sx = trow + X * kKeys + kHalf * q;    // this half's scores / P
+        const uint32_t ox = trow + kOCol + X * D + (D / 2) * q;  // this half's columns of O
         const ScoreMods& md = p.mods;
-        const float sl2 = md.scale_log2;
-        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         int J = 0;             // key tiles of the CTA (the rings' count)
         int items = 0, tiles = 0;  // items and key tiles of this tile X
         bool ok = true;
@@ -542,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lo = live_row ? first_key(md, it.s, pos) : 0;
             const int hi = live_row ? end_key(md, it.s, pos, it.n) : 0x7fffffff;
             const float slope2 = kBias ? md.slopes[head] * kScoreLog2e : 0.f;
-            float m_used = -INFINITY, l = 0.f;
+            float m_used = kFixed ? 0.f : -INFINITY, l = 0.f;
             for (int j = 0; j < it.nkv; ++j, ++J, ++tiles) {
                 const int b = J & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(&s_full[X], tiles & 1, abort_flag, p.status));
@@ -551,138 +614,156 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mbar_wait(&v_full[b], (J >> 1) & 1, abort_flag, p.status));
                 if (!ok) break;
                 tc_fence_after();
-                const unsigned bad = (unsigned)vbad[b];              // 8 blocks of the tile
-                const int key0 = it.b0 * PKV_BLOCK_SIZE + kKeys * j;
+                const unsigned bad = ((unsigned)vbad[b] >> (4 * q)) & 0xFu;  // this half's blocks
+                const int key0 = it.b0 * PKV_BLOCK_SIZE + kKeys * j + kHalf * q;
                 const bool whole = bad == 0u && __all_sync(0xffffffffu, key0 >= lo &&
-                                                                            key0 + kKeys <= hi);
-                float sc[kKeys];
+                                                                            key0 + kHalf <= hi);
+                // keys of chunk w (32 keys) that this row sees
+                auto seen = [&](int w) -> uint32_t {
+                    const int f0 = min(max(lo - key0 - 32 * w, 0), 32);
+                    const int f1 = min(max(hi - key0 - 32 * w, 0), 32);
+                    uint32_t see = (f1 == 32 ? 0xffffffffu : (1u << f1) - 1u) &
+                                   (f0 == 32 ? 0u : 0xffffffffu << f0);
+                    if ((bad >> (2 * w)) & 1u) see &= 0xffff0000u;
+                    if ((bad >> (2 * w + 1)) & 1u) see &= 0x0000ffffu;
+                    return see;
+                };
+                uint64_t acc2[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+                float f = 1.f;  // factor on what the row has so far
+                if constexpr (kFixed) {
+                    // |z| <= cap' <= kFixedMax: weights 2^z fit bf16 and their sums
+                    // fp32 without a maximum taken out
+#pragma unroll 1
+                    for (int w = 0; w < kHalf / 32; ++w) {
+                        float sc[32];
+                        tc_ld32(sx + 32 * w, reinterpret_cast<uint32_t(&)[32]>(sc));
+                        tc_wait_ld();
+                        cap_to_z(p, sc);
+                        if (!whole) {
+                            const uint32_t see = seen(w);
 #pragma unroll
-                for (int q4 = 0; q4 < kKeys / 32; ++q4)
-                    tc_ld32(sx + 32 * q4, reinterpret_cast<uint32_t(&)[32]>(sc[32 * q4]));
-                tc_wait_ld();
-                // sc becomes z / mul (base-2 scores z): raw scores, or
-                // raw * tanh(x) / x with x = raw * cap_in, or z itself
-                float mul = sl2;
-                if constexpr (kCap) {
-                    float ab[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < kKeys; c += 2)
-                        ab[(c >> 1) & 3] = max3(ab[(c >> 1) & 3], fabsf(sc[c]), fabsf(sc[c + 1]));
-                    const float big = fmaxf(fmaxf(ab[0], ab[1]), fmaxf(ab[2], ab[3]));
-                    if (__all_sync(0xffffffffu, big <= p.tanh_limit)) {
-                        uint64_t tc[kTanhTerms];
-#pragma unroll
-                        for (int k = 0; k < kTanhTerms; ++k) tc[k] = f2(p.tanh_c[k], p.tanh_c[k]);
-#pragma unroll
-                        for (int c = 0; c < kKeys; c += 2) {
-                            const uint64_t x = f2(sc[c], sc[c + 1]), v = f2_mul(x, x);
-                            uint64_t y = f2_fma(tc[4], v, tc[3]);
-                            y = f2_fma(y, v, tc[2]);
-                            y = f2_fma(y, v, tc[1]);
-                            y = f2_fma(y, v, tc[0]);
-                            f2_split(f2_mul(x, y), sc[c], sc[c + 1]);
+                            for (int c = 0; c < 32; ++c)
+                                sc[c] = (see >> c) & 1u ? sc[c] : -INFINITY;
                         }
-                    } else {
-                        // z = cap' tanh(x) = cap' - 2 cap' / (1 + e^2x)
-                        const float k2 = 2.f * kScoreLog2e * md.cap_in;
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int c = 0; c < kKeys; ++c)
-                            sc[c] = fmaf(-2.f * md.cap_out, fast_rcp(1.f + fast_exp2(k2 * sc[c])),
-                                         md.cap_out);
+                        for (int e = 0; e < 16; ++e) {
+                            const float p0 = fast_exp2(sc[2 * e]), p1 = fast_exp2(sc[2 * e + 1]);
+                            acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
+                            pk[e] = E::pack(p0, p1);
+                        }
+                        tc_st16(sx + 16 * w, pk);
+                    }
+                } else {
+                    float sc[kHalf];
+                    tc_ld32(sx, reinterpret_cast<uint32_t(&)[32]>(sc[0]));
+                    tc_ld32(sx + 32, reinterpret_cast<uint32_t(&)[32]>(sc[32]));
+                    tc_wait_ld();
+                    // sc becomes z / mul (z: base-2 scores), with mul > 0
+                    float mul = md.scale_log2;
+                    if constexpr (kCap) {
+                        cap_to_z(p, reinterpret_cast<float(&)[32]>(sc[0]));
+                        cap_to_z(p, reinterpret_cast<float(&)[32]>(sc[32]));
                         mul = 1.f;
                     }
-                }
-                if constexpr (kBias) {
-                    // distance |p - t|: keys before the row's position for all but
-                    // the tiles at the diagonal or in a prefix
-                    if (__all_sync(0xffffffffu, key0 + kKeys - 1 <= pos)) {
-                        const float base = slope2 * (float)(key0 - pos);
+                    if constexpr (kBias) {
+                        // distance |p - t|: keys before the row's position for all but
+                        // the tiles at the diagonal or in a prefix
+                        const uint64_t mul2 = f2(mul, mul);
+                        if (__all_sync(0xffffffffu, key0 + kHalf - 1 <= pos)) {
+                            const float base = slope2 * (float)(key0 - pos);
 #pragma unroll
-                        for (int c = 0; c < kKeys; c += 2) {
-                            const uint64_t bb = f2(fmaf(slope2, (float)c, base),
-                                                   fmaf(slope2, (float)(c + 1), base));
-                            f2_split(f2_fma(f2(sc[c], sc[c + 1]), f2(mul, mul), bb), sc[c],
-                                     sc[c + 1]);
+                            for (int c = 0; c < kHalf; c += 2) {
+                                const uint64_t bb = f2(fmaf(slope2, (float)c, base),
+                                                       fmaf(slope2, (float)(c + 1), base));
+                                f2_split(f2_fma(f2(sc[c], sc[c + 1]), mul2, bb), sc[c], sc[c + 1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < kHalf; ++c)
+                                sc[c] = fmaf(-slope2, fabsf((float)(key0 + c - pos)), sc[c] * mul);
                         }
-                    } else {
+                        mul = 1.f;
+                    } else if (mul <= 0.f) {
 #pragma unroll
-                        for (int c = 0; c < kKeys; ++c)
-                            sc[c] = fmaf(-slope2, fabsf((float)(key0 + c - pos)), sc[c] * mul);
+                        for (int c = 0; c < kHalf; ++c) sc[c] *= mul;
+                        mul = 1.f;
                     }
-                    mul = 1.f;
-                } else if (mul <= 0.f) {  // a maximum of z / mul needs mul > 0
+                    if (!whole) {  // select: hidden scores may be anything
 #pragma unroll
-                    for (int c = 0; c < kKeys; ++c) sc[c] *= mul;
-                    mul = 1.f;
-                }
-                if (!whole) {  // select: hidden scores may be anything
-                    const int a = lo - key0, e = hi - key0;  // visible: a <= c < e
+                        for (int w = 0; w < kHalf / 32; ++w) {
+                            const uint32_t see = seen(w);
 #pragma unroll
-                    for (int w = 0; w < kKeys / 32; ++w) {
-                        const int f0 = min(max(a - 32 * w, 0), 32), f1 = min(max(e - 32 * w, 0), 32);
-                        uint32_t see = (f1 == 32 ? 0xffffffffu : (1u << f1) - 1u) &
-                                       (f0 == 32 ? 0u : 0xffffffffu << f0);
-                        if ((bad >> (2 * w)) & 1u) see &= 0xffff0000u;
-                        if ((bad >> (2 * w + 1)) & 1u) see &= 0x0000ffffu;
+                            for (int c = 0; c < 32; ++c)
+                                sc[32 * w + c] = (see >> c) & 1u ? sc[32 * w + c] : -INFINITY;
+                        }
+                    }
+                    float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            sc[32 * w + c] = (see >> c) & 1u ? sc[32 * w + c] : -INFINITY;
+                    for (int c = 0; c < kHalf; c += 2)
+                        mxp[(c >> 1) & 3] = max3(mxp[(c >> 1) & 3], sc[c], sc[c + 1]);
+                    float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mul;
+                    // the row's maximum over both halves
+                    float* mine = xm + (((tiles & 1) * 2 + X) * 2 + q) * kRows + r;
+                    *mine = mx;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x_max[4 * X + wq]);
+                    ok = __all_sync(0xffffffffu, mbar_wait(&x_max[4 * X + wq], tiles & 1,
+                                                           abort_flag, p.status));
+                    if (!ok) break;
+                    mx = fmaxf(mx, *(mine + (q ? -kRows : kRows)));
+                    const float m_new = fmaxf(m_used, mx);
+                    // lazy rescale: only when the maximum grew by more than 2^kRescale
+                    const bool grow = m_used != -INFINITY && m_new > m_used + kRescale;
+                    f = grow ? fast_exp2(m_used - m_new) : 1.f;
+                    if (m_used == -INFINITY || grow) m_used = m_new;
+                    const float ms = m_used == -INFINITY ? 0.f : m_used;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        // S_X(J) was issued after P V_X(J-1): O_X holds every earlier tile
+#pragma unroll 1
+                        for (int c = 0; c < D / 64; ++c) {
+                            uint32_t o[32];
+                            tc_ld32(ox + 32 * c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc_st32(ox + 32 * c, o);
+                        }
+                    }
+                    // P as 16-bit pairs (every score is in registers); the sum takes
+                    // the unrounded weights
+                    const uint64_t mul2 = f2(mul, mul), nms2 = f2(-ms, -ms);
+#pragma unroll
+                    for (int w = 0; w < kHalf / 32; ++w) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float a0, a1;
+                            f2_split(f2_fma(f2(sc[32 * w + 2 * e], sc[32 * w + 2 * e + 1]), mul2,
+                                            nms2),
+                                     a0, a1);
+                            const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                            acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
+                            pk[e] = E::pack(p0, p1);
+                        }
+                        tc_st16(sx + 16 * w, pk);
                     }
                 }
-                float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float psum = 0.f;
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 2)
-                    mxp[(c >> 1) & 3] = max3(mxp[(c >> 1) & 3], sc[c], sc[c + 1]);
-                const float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mul;
-                const float m_new = fmaxf(m_used, mx);
-                // lazy rescale: only when the maximum grew by more than 2^kRescale
-                const bool grow = m_used != -INFINITY && m_new > m_used + kRescale;
-                const float f = grow ? fast_exp2(m_used - m_new) : 1.f;
-                if (m_used == -INFINITY || grow) m_used = m_new;
-                const float ms = m_used == -INFINITY ? 0.f : m_used;
-                if (__any_sync(0xffffffffu, grow)) {
-                    // S_X(J) was issued after P V_X(J-1): O_X holds every earlier tile
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tc_ld32(ox + 32 * c, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc_st32(ox + 32 * c, o);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    float a0, a1;
+                    f2_split(acc2[e], a0, a1);
+                    psum += a0 + a1;
                 }
-                // P as 16-bit pairs over the first 64 columns (every score is in
-                // registers); the sum takes the unrounded weights
-                const uint64_t mul2 = f2(mul, mul), nms2 = f2(-ms, -ms);
-                uint64_t acc2[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-                for (int c4 = 0; c4 < kKeys / 32; ++c4) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float a0, a1;
-                        f2_split(f2_fma(f2(sc[32 * c4 + 2 * e], sc[32 * c4 + 2 * e + 1]), mul2,
-                                        nms2),
-                                 a0, a1);
-                        const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-                        acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
-                        pk[e] = E::pack(p0, p1);
-                    }
-                    tc_st16(sx + 16 * c4, pk);
-                }
-                float psp[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f2_split(acc2[e], psp[2 * e], psp[2 * e + 1]);
-                const float psum = ((psp[0] + psp[1]) + (psp[2] + psp[3])) +
-                                   ((psp[4] + psp[5]) + (psp[6] + psp[7]));
                 tc_wait_st();
                 l = l * f + psum;
                 // V rows that no row of the item sees (or that were not loaded)
                 // become zeros before P V; both tiles zero the same rows
                 if (j == 0 || j == it.nkv - 1 || bad) {
-                    unsigned char* vt = sv + b * TILE;
-                    for (int x = r; x < kKeys * 8 * HALVES; x += kRows) {
+                    unsigned char* vt = sv + b * TILE + kHalf * q * 128;
+                    for (int x = r; x < kHalf * 8 * HALVES; x += kRows) {
                         const int kq = x / (8 * HALVES), rest = x - kq * (8 * HALVES);
                         const int key = key0 + kq;
                         if (key >= it.lo && key < it.hi && !((bad >> (kq >> 4)) & 1u)) continue;
@@ -693,79 +774,85 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                 tc_fence_before();  // P and a rescaled O are ordered before the next MMA
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[X]);
+                if (lane == 0) mbar_arrive(&p_full[2 * X + q]);
             }
             if (!ok) break;
-            // ---- epilogue: O_X / l for the rows of the chunk, or their partials
+            // ---- epilogue: O_X / l (this half's columns) for the rows of the chunk,
+            // or their partials
             const bool split = p.splits > 1;
-            T* dst = static_cast<T*>(p.out) +
-                     ((size_t)(it.q0 + (live_row ? t : 0)) * Hq + head) * D;
+            const size_t orow = (size_t)(it.q0 + (live_row ? t : 0)) * Hq + head;
+            T* dst = static_cast<T*>(p.out) + orow * D + (D / 2) * q;
             const size_t prow =
                 ((size_t)it.base * p.splits + it.split) * kPair + X * kRows + r;
-            if (split && live_row) {
-                p.ws_m[prow] = m_used;
-                p.ws_l[prow] = l;
-            }
-            if (it.nkv == 0) {  // nothing visible: zeros (a split's joiner skips it: l = 0)
+            if (it.nkv == 0) {  // nothing visible: zeros, or an empty partial (l = 0)
+                if (live_row && split && q == 0) {
+                    p.ws_m[prow] = -INFINITY;
+                    p.ws_l[prow] = 0.f;
+                }
                 if (live_row && !split)
-                    for (int c = 0; c < D / 8; ++c)
+                    for (int c = 0; c < D / 16; ++c)
                         *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
                 continue;
             }
-            const float inv = l != 0.f ? 1.f / l : 0.f;
             ok = __all_sync(0xffffffffu, mbar_wait(&o_ready[X], items & 1, abort_flag, p.status));
             if (!ok) break;
             tc_fence_after();
-            bool finite = true;
+            float o[D / 2];
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tc_ld32(ox + 32 * c, o);
-                tc_wait_ld();
-                float sum = 0.f;  // finite values times zero: NaN if one is not finite
+            for (int c = 0; c < D / 64; ++c)
+                tc_ld32(ox + 32 * c, reinterpret_cast<uint32_t(&)[32]>(o[32 * c]));
+            tc_wait_ld();
+            tc_fence_before();
+            float zero = 0.f;  // finite values times zero: NaN if one is not finite
 #pragma unroll
-                for (int e = 0; e < 32; ++e) sum = fmaf(0.f, __uint_as_float(o[e]), sum);
-                finite = finite && sum == 0.f;
-                if (!live_row) continue;
+            for (int e = 0; e < D / 2; ++e) zero = fmaf(0.f, o[e], zero);
+            float* mine = xl + (((items & 1) * 2 + X) * 2 + q) * kRows + r;
+            *mine = l + zero;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&o_free[X]);
+                mbar_arrive(&x_sum[4 * X + wq]);
+            }
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(&x_sum[4 * X + wq], items & 1, abort_flag, p.status));
+            if (!ok) break;
+            ++items;
+            l = *mine + *(mine + (q ? -kRows : kRows));
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            // rows that met something not finite are computed again below
+            const bool clean = l - l == 0.f;
+            if (live_row && clean) {
                 if (split) {
-                    float* od = p.ws_o + prow * D + 32 * c;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w8[8];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) w8[u] = o[8 * e + u];
-                        st_global_v8(od + 8 * e, w8);
+                    if (q == 0) {
+                        p.ws_m[prow] = m_used;
+                        p.ws_l[prow] = l;
                     }
-                    continue;
-                }
-                uint32_t w[16];
+                    float* od = p.ws_o + prow * D + (D / 2) * q;
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    w[u] = l != 0.f ? E::pack(__uint_as_float(o[2 * u]) * inv,
-                                              __uint_as_float(o[2 * u + 1]) * inv)
-                                    : 0u;
-                if (out32) {
-                    // 32-byte stores: each fills a whole L2 sector
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t w8[8];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) w8[u] = w[8 * hh + u];
-                        st_global_v8(dst + 32 * c + 16 * hh, w8);
-                    }
+                    for (int e = 0; e < D / 8; ++e)
+                        *reinterpret_cast<float4*>(od + 4 * e) =
+                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<uint4*>(dst + 32 * c + 8 * e) =
-                            make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t w8[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            w8[u] = E::pack(o[16 * c + 2 * u] * inv, o[16 * c + 2 * u + 1] * inv);
+                        if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+                            st_global_v8(dst + 16 * c, w8);  // a whole L2 sector
+                        } else {
+                            *reinterpret_cast<uint4*>(dst + 16 * c) =
+                                make_uint4(w8[0], w8[1], w8[2], w8[3]);
+                            *reinterpret_cast<uint4*>(dst + 16 * c + 8) =
+                                make_uint4(w8[4], w8[5], w8[6], w8[7]);
+                        }
+                    }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free[X]);
-            ++items;
-            // rows that met something not finite: again, from their own keys
-            unsigned redo = __ballot_sync(0xffffffffu, live_row && l != 0.f && !finite);
+            // again, by the whole warp and from the row's own keys (each half
+            // stores its columns)
+            unsigned redo = __ballot_sync(0xffffffffu, live_row && !clean);
             while (redo) {
                 const int who = __ffs(redo) - 1;
                 redo &= redo - 1;
@@ -774,23 +861,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int klo = max(first_key(md, it.s, pos2), it.b0 * PKV_BLOCK_SIZE);
                 const int khi = min(end_key(md, it.s, pos2, it.n),
                                     (it.b0 + it.nblk) * PKV_BLOCK_SIZE);
-                float o[D / 32], m2, l2;
-                plain_row<T, D>(p, it.s, it.h, head2, it.q0 + t2, pos2, klo, khi, o, m2, l2);
+                float o2[D / 32], m2, l2;
+                plain_row<T, D>(p, it.s, it.h, head2, it.q0 + t2, pos2, klo, khi, o2, m2, l2);
                 const size_t prow2 = prow - lane + who;
                 T* dst2 = static_cast<T*>(p.out) + ((size_t)(it.q0 + t2) * Hq + head2) * D;
                 const float inv2 = l2 != 0.f ? 1.f / l2 : 0.f;
+                if (lane / 16 == q) {
 #pragma unroll
-                for (int e = 0; e < D / 32; e += 2) {
-                    const int d = lane * (D / 32) + e;
-                    if (split) {
-                        p.ws_o[prow2 * D + d] = o[e];
-                        p.ws_o[prow2 * D + d + 1] = o[e + 1];
-                    } else {
-                        *reinterpret_cast<uint32_t*>(dst2 + d) =
-                            E::pack(o[e] * inv2, o[e + 1] * inv2);
+                    for (int e = 0; e < D / 32; e += 2) {
+                        const int d = lane * (D / 32) + e;
+                        if (split) {
+                            p.ws_o[prow2 * D + d] = o2[e];
+                            p.ws_o[prow2 * D + d + 1] = o2[e + 1];
+                        } else {
+                            *reinterpret_cast<uint32_t*>(dst2 + d) =
+                                E::pack(o2[e] * inv2, o2[e + 1] * inv2);
+                        }
                     }
                 }
-                if (split && lane == 0) {
+                if (split && lane == 0 && q == 0) {
                     p.ws_m[prow2] = m2;
                     p.ws_l[prow2] = l2;
                 }
@@ -882,14 +971,15 @@ Workspace ws_layout(long long rows, int head_dim) {
 
 template <int D>
 size_t prefill_smem() {
-    // 2 Q tiles, 2 K and 2 V stages, barriers (under 1 KB); 1 KB alignment slack
-    return 1024 + (size_t)6 * (D / 64) * kRows * 128 + 1024;
+    // 2 Q tiles, 2 K and 2 V stages, barriers (under 1 KB) and the halves'
+    // maxima and sums (4 KB each); 1 KB alignment slack
+    return 1024 + (size_t)6 * (D / 64) * kRows * 128 + 1024 + 2 * 2 * 2 * 2 * kRows * 4;
 }
 
-template <typename T, int D, bool kCap, bool kBias>
+template <typename T, int D, bool kCap, bool kBias, bool kFixed = false>
 pkv_status launch(const PrefillScored& prm, const CUtensorMap& tmk, const CUtensorMap& tmv,
                   const CUtensorMap& tmq, int q_tma, int items, int ctas, cudaStream_t stream) {
-    auto kern = scored_prefill_kernel<T, D, kCap, kBias>;
+    auto kern = scored_prefill_kernel<T, D, kCap, kBias, kFixed>;
     // the register shares assume the launch count of this build
     static const bool regs_ok = [&] {
         cudaFuncAttributes a;
@@ -919,6 +1009,10 @@ pkv_status launch_mods(const PrefillScored& prm, pkv_dtype dtype, int items, int
         make_q_tile_map(&tmq, prm.q, prm.num_q_rows, prm.num_q_heads, D, prm.group, dtype) ? 1 : 0;
     if (!q_tma) tmq = tmk;  // unused
     const bool cap = prm.mods.cap_out > 0.f, bias = prm.mods.slopes != nullptr;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        if (cap && !bias && prm.mods.cap_out <= kFixedMax)
+            return launch<T, D, true, false, true>(prm, tmk, tmv, tmq, q_tma, items, ctas, stream);
+    }
     if (cap)
         return bias ? launch<T, D, true, true>(prm, tmk, tmv, tmq, q_tma, items, ctas, stream)
                     : launch<T, D, true, false>(prm, tmk, tmv, tmq, q_tma, items, ctas, stream);
@@ -1000,19 +1094,18 @@ pkv_status paged_attention_prefill_scored(
     prm.num_q_rows = num_q_rows;
     prm.pairs_per_seq = pl.pairs;
     prm.splits = pl.splits;
-    // the polynomial's terms for raw scores: tanh(x) / x = sum c_i x^2i, x = raw cap_in
+    // z = cap' x (tanh(x) / x) with x = raw cap_in: the terms in raw^2, times cap' cap_in
     prm.tanh_limit = -1.f;
     if (softcap > 0.f && scale != 0.f) {
         const double c2 = (double)prm.mods.cap_in * prm.mods.cap_in;
         double f = 1.0;
         bool ok = true;
         for (int i = 0; i < pkv::kTanhTerms; ++i, f *= c2) {
-            prm.tanh_c[i] = (float)(pkv::tanh_term(i) * f);
-            ok = ok && std::isnormal(prm.tanh_c[i]);
+            prm.tanh_z[i] = (float)(pkv::tanh_term(i) * f * prm.mods.scale_log2);
+            ok = ok && std::isnormal(prm.tanh_z[i]);
         }
-        const float limit = pkv::kTanhRange / std::fabs(prm.mods.cap_in);
-        // raw^2 must stay finite too
-        if (ok && limit < 1e18f) prm.tanh_limit = limit;
+        const double limit = pkv::kTanhRange * pkv::kTanhRange / c2;
+        if (ok && std::isnormal((float)limit)) prm.tanh_limit = (float)limit;
     }
     const pkv::Workspace ws =
         pkv::ws_layout(pl.splits > 1 ? pl.items * pl.splits * pkv::kPair : 0, head_dim);
