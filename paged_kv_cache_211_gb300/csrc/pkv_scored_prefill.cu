@@ -7,7 +7,7 @@
 // cap, bias and exp2.  With a cap the scores, not the products, bound it: the
 // special-function pipe does tanh as exp2 and a reciprocal, three results a
 // score with the softmax's own exp2.  So a tile whose scores all lie within
-// |z / cap| <= 0.75 takes tanh from a polynomial on the (packed, two a cycle)
+// |z / cap| <= 0.5 takes tanh from a polynomial on the (packed, two a cycle)
 // fp32 pipe instead, and only the others from exp2 and the reciprocal.
 //
 // Work item: one sequence, one KV head, a pair of 128-row tiles A and B (256
@@ -58,12 +58,12 @@ static_assert(128 * kOtherRegs + kSoftWarps * 32 * kSoftmaxRegs <= kThreads * kL
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// tanh(x) / x on |x| <= 0.75 as a polynomial in x^2: fitted here by iterated
-// weighted least squares to the smallest largest relative error, 5.7e-7.
-constexpr float kTanhRange = 0.75f;
-constexpr int kTanhTerms = 5;
+// tanh(x) / x on |x| <= 0.5 as a polynomial in x^2: fitted here by iterated
+// weighted least squares to the smallest largest relative error, 5.5e-7.
+constexpr float kTanhRange = 0.5f;
+constexpr int kTanhTerms = 4;
 __host__ __device__ constexpr float tanh_term(int i) {
-    return i == 0 ? 0.999999435f : i == 1 ? -0.333282515f : i == 2 ? 0.132589832f : i == 3 ? -0.0500563026f : 0.0129296324f;
+    return i == 0 ? 0.999999456f : i == 1 ? -0.333263179f : i == 2 ? 0.131902966f : -0.0444022261f;
 }
 
 struct PrefillScored {
@@ -88,14 +88,20 @@ struct PrefillScored {
     float* ws_o;           // [row][D]
 };
 
-struct Item {
+struct __align__(16) Item {
     int s, h, q0, qlen, n, row0;
     int split, base;       // base: item without its split
     int lo, hi;            // keys that some row of the item sees
     int b0, nblk;          // this split's first block and its number of blocks
-    int nkv;               // its key tiles (0: nothing to compute)
-    bool has_b;            // tile B holds rows
+    int nkv;               // its key tiles (0: nothing to compute; -1: no item)
+    int has_b;             // tile B holds rows
+    int start, prefix;     // the sequence's first key, and its prefix (at most n)
 };
+static_assert(sizeof(Item) == 64, "four 16-byte words");
+// Rounds whose items a CTA works out at its start, one thread each (an item
+// takes a dozen divisions and dependent loads: 11 800 cycles went by between an
+// item's last key tile and the next one's first when every role did it by itself)
+constexpr int kItemCache = 256;
 
 // A sequence's chunk is usable if its rows lie inside q and out, it is no
 // longer than the host bound, and it fits its context and the table.
@@ -104,11 +110,11 @@ __device__ __forceinline__ bool lengths_ok(const PrefillScored& p, int q0, int q
            n <= p.max_blocks_per_seq * PKV_BLOCK_SIZE;
 }
 
-// Keys hidden behind a prefix end at this bound for the query at position p.
-__device__ __forceinline__ int end_key(const ScoreMods& m, int s, int p, int n) {
-    const int pre = m.prefix_lens ? min(m.prefix_lens[s], n) : 0;
-    return max(p + 1, pre);
+// The visible keys [lo, hi) of the row at position pos.
+__device__ __forceinline__ int row_lo(const PrefillScored& p, const Item& it, int pos) {
+    return p.mods.window > 0 ? max(it.start, pos - p.mods.window + 1) : it.start;
 }
+__device__ __forceinline__ int row_hi(const Item& it, int pos) { return max(pos + 1, it.prefix); }
 
 // Item i, heaviest first (pairs from the end of each chunk, where the causal
 // range is longest); false if it holds no rows or its lengths are invalid
@@ -125,6 +131,7 @@ __device__ __forceinline__ bool item_at(const PrefillScored& p, int i, bool flag
     it.q0 = p.cu_q_lens[it.s];
     it.qlen = p.cu_q_lens[it.s + 1] - it.q0;
     it.n = p.context_lens[it.s];
+    it.nkv = -1;
     if (!lengths_ok(p, it.q0, it.qlen, it.n)) {
         if (flag && pair == 0 && it.h == 0 && it.split == 0 && it.qlen != 0)
             atomicOr(p.status, PKV_DEV_BAD_LENGTH);
@@ -137,8 +144,10 @@ __device__ __forceinline__ bool item_at(const PrefillScored& p, int i, bool flag
     const int t_first = it.row0 / g;
     const int t_last = min(it.qlen, (it.row0 + kPair + g - 1) / g) - 1;
     const int base_pos = it.n - it.qlen;
-    it.lo = first_key(p.mods, it.s, base_pos + t_first);
-    it.hi = end_key(p.mods, it.s, base_pos + t_last, it.n);
+    it.start = p.mods.key_starts ? max(p.mods.key_starts[it.s], 0) : 0;
+    it.prefix = p.mods.prefix_lens ? min(p.mods.prefix_lens[it.s], it.n) : 0;
+    it.lo = row_lo(p, it, base_pos + t_first);
+    it.hi = row_hi(it, base_pos + t_last);
     it.b0 = it.lo / PKV_BLOCK_SIZE;
     it.nblk = it.nkv = 0;
     if (it.lo >= it.hi) return true;
@@ -157,6 +166,17 @@ __device__ __forceinline__ bool item_at(const PrefillScored& p, int i, bool flag
 __device__ __forceinline__ int round_item(int r) {
     const int G = gridDim.x, c = blockIdx.x;
     return r * G + ((r & 1) ? G - 1 - c : c);
+}
+
+// The item of round r from the CTA's table (past it: worked out again); false: none.
+__device__ __forceinline__ bool round_at(const PrefillScored& p, const Item* table, int num_items,
+                                         int r, bool flag, Item& it) {
+    if (r < kItemCache) {
+        it = table[r];
+        return it.nkv >= 0;
+    }
+    const int i = round_item(r);
+    return i < num_items && item_at(p, i, flag, it);
 }
 
 // Two-wide fp32 arithmetic on packed register pairs, the three-input maximum
@@ -203,11 +223,10 @@ __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&w)[8]) 
 
 // One row again, by a whole warp and from its own keys only (keys [lo, hi) of
 // its sequence): a key it does not see, or whose block id is bad, is never
-// read.  Lane x gets elements x * D / 32 .. of the unnormalised output.
+// read.  Lane x gets elements x * D / 32 .. of the (normalised) output.
 template <typename T, int D>
-__device__ __noinline__ void plain_row(const PrefillScored& p, int s, int h, int head, int row,
-                                       int pos, int lo, int hi, float (&o)[D / 32], float& m,
-                                       float& l) {
+__device__ void plain_row(const PrefillScored& p, int s, int h, int head, int row, int pos, int lo,
+                          int hi, float (&o)[D / 32]) {
     constexpr int PER = D / 32;
     const int lane = threadIdx.x & 31;
     const T* q = static_cast<const T*>(p.q) + ((size_t)row * p.num_q_heads + head) * D;
@@ -217,8 +236,7 @@ __device__ __noinline__ void plain_row(const PrefillScored& p, int s, int h, int
     const int32_t* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
     const ScoreMods& md = p.mods;
     const float slope = md.slopes ? md.slopes[head] * kScoreLog2e : 0.f;
-    m = -INFINITY;
-    l = 0.f;
+    float m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int e = 0; e < PER; ++e) o[e] = 0.f;
     for (int t0 = lo; t0 < hi; t0 += 32) {
@@ -257,6 +275,39 @@ __device__ __noinline__ void plain_row(const PrefillScored& p, int s, int h, int
             for (int e = 0; e < PER; ++e) o[e] = fmaf(wx, (float)v[e], o[e]);
         }
     }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] *= inv;
+}
+
+// Replaces column half q of the rows row0 + (bit of `which`) of an item, whose
+// O met something not finite; l: the lane's row's sum, which their partials are
+// relative to.
+template <typename T, int D>
+__device__ __noinline__ void redo_rows(const PrefillScored& p, const Item& it, int row0, int q,
+                                       unsigned which, float l, size_t prow0) {
+    const int lane = threadIdx.x & 31, g = p.group;
+    while (which) {
+        const int who = __ffs(which) - 1;
+        which &= which - 1;
+        const int R = row0 + who, t = R / g, head = it.h * g + R - t * g;
+        const int pos = it.n - it.qlen + t;
+        const int lo = max(row_lo(p, it, pos), it.b0 * PKV_BLOCK_SIZE);
+        const int hi = min(row_hi(it, pos), (it.b0 + it.nblk) * PKV_BLOCK_SIZE);
+        float o[D / 32];
+        plain_row<T, D>(p, it.s, it.h, head, it.q0 + t, pos, lo, hi, o);
+        const float lw = __shfl_sync(0xffffffffu, l, who);
+        if (lane / 16 != q) continue;
+        const int d = lane * (D / 32);
+        if (p.splits > 1) {
+            for (int e = 0; e < D / 32; ++e) p.ws_o[(prow0 + who) * D + d + e] = o[e] * lw;
+        } else {
+            T* dst = static_cast<T*>(p.out) + ((size_t)(it.q0 + t) * p.num_q_heads + head) * D + d;
+#pragma unroll
+            for (int e = 0; e < D / 32; e += 2)
+                *reinterpret_cast<uint32_t*>(dst + e) = Elem<T>::pack(o[e], o[e + 1]);
+        }
+    }
 }
 
 // 32 raw scores to capped base-2 scores z = cap' tanh(raw cap_in), cap' = cap
@@ -274,16 +325,13 @@ __device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[32]
         top[e & 1] = max3(top[e & 1], a0, a1);
     }
     if (__all_sync(0xffffffffu, fmaxf(top[0], top[1]) <= p.tanh_limit)) {
-        const uint64_t c4 = f2(p.tanh_z[4], p.tanh_z[4]), c3 = f2(p.tanh_z[3], p.tanh_z[3]);
-        const uint64_t c2 = f2(p.tanh_z[2], p.tanh_z[2]), c1 = f2(p.tanh_z[1], p.tanh_z[1]);
-        const uint64_t c0 = f2(p.tanh_z[0], p.tanh_z[0]);
+        const uint64_t c3 = f2(p.tanh_z[3], p.tanh_z[3]), c2 = f2(p.tanh_z[2], p.tanh_z[2]);
+        const uint64_t c1 = f2(p.tanh_z[1], p.tanh_z[1]), c0 = f2(p.tanh_z[0], p.tanh_z[0]);
 #pragma unroll
         for (int e0 = 0; e0 < 16; e0 += 4) {  // four independent chains at a time
             uint64_t y[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = f2_fma(c4, v[e0 + u], c3);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[e0 + u], c2);
+            for (int u = 0; u < 4; ++u) y[u] = f2_fma(c3, v[e0 + u], c2);
 #pragma unroll
             for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[e0 + u], c1);
 #pragma unroll
@@ -337,9 +385,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vbad + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     // what the two key halves of a row tell each other, by parity:
-    // [parity][tile][half][row] maxima, and sums (NaN: O is not finite)
+    // [parity][tile][half][row] maxima, and sums
     float* xm = reinterpret_cast<float*>(tmem_slot + 2);
     float* xl = xm + 2 * 2 * 2 * kRows;
+    Item* table = reinterpret_cast<Item*>(
+        (reinterpret_cast<uintptr_t>(xl + 2 * 2 * 2 * kRows) + 15) & ~(uintptr_t)15);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = p.group, Hq = p.num_q_heads;
@@ -367,11 +417,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 2) tc_alloc(tmem_slot, kCols);
+    const int rounds = (num_items + (int)gridDim.x - 1) / (int)gridDim.x;
+    if (tid < min(rounds, kItemCache)) {
+        Item it;
+        it.nkv = -1;
+        const int i = round_item(tid);
+        if (i < num_items) item_at(p, i, true, it);
+        table[tid] = it;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int rounds = (num_items + (int)gridDim.x - 1) / (int)gridDim.x;
     // whole warpgroups: warps 0-3 release registers, 4-11 take them
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
@@ -385,9 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int J = 0;  // key tiles issued by this CTA
         bool live = true;
         for (int rd = 0; rd < rounds && live; ++rd) {
-            const int i = round_item(rd);
             Item it;
-            if (i >= num_items || !item_at(p, i, isk && lane == 0, it)) continue;
+            if (!round_at(p, table, num_items, rd, isk && lane == 0, it)) continue;
             const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks_per_seq + it.b0;
             for (int j = 0; j < it.nkv; ++j, ++J) {
                 const int b = J & 1, ph = (J >> 1) & 1;
@@ -429,9 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int issued[2] = {0, 0};    // items whose tile X was loaded
         bool live = true;
         for (int rd = 0; rd < rounds && live; ++rd) {
-            const int i = round_item(rd);
             Item it;
-            if (i >= num_items || !item_at(p, i, false, it) || it.nkv == 0) continue;
+            if (!round_at(p, table, num_items, rd, false, it) || it.nkv == 0) continue;
             for (int X = 0; X < (it.has_b ? 2 : 1) && live; ++X) {
                 live = __all_sync(0xffffffffu, mbar_wait(&q_empty[X], (issued[X] & 1) ^ 1,
                                                          abort_flag, p.status));
@@ -445,6 +500,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int hh = 0; hh < HALVES; ++hh)
                             tma_load_rows(sq + X * TILE + hh * REG, &tmap_q, &q_full[X], hh * 64,
                                           it.h * g, it.q0 + row / g);
+                        // the next round's tile into L2 meanwhile
+                        Item nx;
+                        if (rd + 1 < min(rounds, kItemCache) &&
+                            round_at(p, table, num_items, rd + 1, false, nx)) {
+#pragma unroll
+                            for (int hh = 0; hh < HALVES; ++hh)
+                                tma_prefetch_rows(&tmap_q, hh * 64, nx.h * g,
+                                                  nx.q0 + (nx.row0 + X * kRows) / g);
+                        }
                     }
                     __syncwarp();
                     continue;
@@ -495,9 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return true;
                 }
                 for (++c.r; c.r < rounds; ++c.r) {
-                    const int i = round_item(c.r);
                     Item it;
-                    if (i >= num_items || !item_at(p, i, false, it) || it.nkv == 0) continue;
+                    if (!round_at(p, table, num_items, c.r, false, it) || it.nkv == 0) continue;
                     c.nkv = it.nkv;
                     c.has_b = it.has_b;
                     c.j = 0;
@@ -586,13 +649,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sx = trow + X * kKeys + kHalf * q;    // this half's scores / P
         const uint32_t ox = trow + kOCol + X * D + (D / 2) * q;  // this half's columns of O
         const ScoreMods& md = p.mods;
+        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         int J = 0;             // key tiles of the CTA (the rings' count)
         int items = 0, tiles = 0;  // items and key tiles of this tile X
         bool ok = true;
         for (int rd = 0; rd < rounds && ok; ++rd) {
-            const int i = round_item(rd);
             Item it;
-            if (i >= num_items || !item_at(p, i, false, it)) continue;
+            if (!round_at(p, table, num_items, rd, false, it)) continue;
             if (X == 1 && !it.has_b) {
                 J += it.nkv;
                 continue;
@@ -602,8 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = it.h * g + (live_row ? R - t * g : 0);
             const int pos = it.n - it.qlen + (live_row ? t : 0);
             // this row's visible keys (rows past the chunk: everything, never stored)
-            const int lo = live_row ? first_key(md, it.s, pos) : 0;
-            const int hi = live_row ? end_key(md, it.s, pos, it.n) : 0x7fffffff;
+            const int lo = live_row ? row_lo(p, it, pos) : 0;
+            const int hi = live_row ? row_hi(it, pos) : 0x7fffffff;
             const float slope2 = kBias ? md.slopes[head] * kScoreLog2e : 0.f;
             float m_used = kFixed ? 0.f : -INFINITY, l = 0.f;
             for (int j = 0; j < it.nkv; ++j, ++J, ++tiles) {
@@ -770,8 +833,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4*>(vt + (rest >> 3) * REG + kq * 128 +
                                                   ((rest & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
                     }
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                 }
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                 tc_fence_before();  // P and a rescaled O are ordered before the next MMA
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[2 * X + q]);
@@ -794,96 +857,71 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
                 continue;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_ready[X], items & 1, abort_flag, p.status));
-            if (!ok) break;
-            tc_fence_after();
-            float o[D / 2];
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-                tc_ld32(ox + 32 * c, reinterpret_cast<uint32_t(&)[32]>(o[32 * c]));
-            tc_wait_ld();
-            tc_fence_before();
-            float zero = 0.f;  // finite values times zero: NaN if one is not finite
-#pragma unroll
-            for (int e = 0; e < D / 2; ++e) zero = fmaf(0.f, o[e], zero);
+            // the row's sum over both halves
             float* mine = xl + (((items & 1) * 2 + X) * 2 + q) * kRows + r;
-            *mine = l + zero;
+            *mine = l;
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&o_free[X]);
-                mbar_arrive(&x_sum[4 * X + wq]);
-            }
+            if (lane == 0) mbar_arrive(&x_sum[4 * X + wq]);
             ok = __all_sync(0xffffffffu,
                             mbar_wait(&x_sum[4 * X + wq], items & 1, abort_flag, p.status));
             if (!ok) break;
-            ++items;
-            l = *mine + *(mine + (q ? -kRows : kRows));
+            l += *(mine + (q ? -kRows : kRows));
             const float inv = l != 0.f ? 1.f / l : 0.f;
-            // rows that met something not finite are computed again below
-            const bool clean = l - l == 0.f;
-            if (live_row && clean) {
-                if (split) {
-                    if (q == 0) {
-                        p.ws_m[prow] = m_used;
-                        p.ws_l[prow] = l;
-                    }
-                    float* od = p.ws_o + prow * D + (D / 2) * q;
+            if (split && live_row && q == 0) {
+                p.ws_m[prow] = m_used;
+                p.ws_l[prow] = l;
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_ready[X], items & 1, abort_flag, p.status));
+            if (!ok) break;
+            ++items;
+            tc_fence_after();
+            float zero = 0.f;  // finite values times zero: NaN if one is not finite
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+                float o[32];
+                tc_ld32(ox + 32 * c, reinterpret_cast<uint32_t(&)[32]>(o));
+                tc_wait_ld();
+                float z4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < D / 8; ++e)
+                for (int e = 0; e < 32; ++e) z4[e & 3] = fmaf(0.f, o[e], z4[e & 3]);
+                zero += (z4[0] + z4[1]) + (z4[2] + z4[3]);
+                if (!live_row) continue;
+                if (split) {
+                    float* od = p.ws_o + prow * D + (D / 2) * q + 32 * c;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
                         *reinterpret_cast<float4*>(od + 4 * e) =
                             make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else {
+                    continue;
+                }
+                uint32_t w[16];
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
+                for (int u = 0; u < 16; ++u) w[u] = E::pack(o[2 * u] * inv, o[2 * u + 1] * inv);
+                if (out32) {  // 32-byte stores: each fills a whole L2 sector
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
                         uint32_t w8[8];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            w8[u] = E::pack(o[16 * c + 2 * u] * inv, o[16 * c + 2 * u + 1] * inv);
-                        if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
-                            st_global_v8(dst + 16 * c, w8);  // a whole L2 sector
-                        } else {
-                            *reinterpret_cast<uint4*>(dst + 16 * c) =
-                                make_uint4(w8[0], w8[1], w8[2], w8[3]);
-                            *reinterpret_cast<uint4*>(dst + 16 * c + 8) =
-                                make_uint4(w8[4], w8[5], w8[6], w8[7]);
-                        }
+                        for (int u = 0; u < 8; ++u) w8[u] = w[8 * hh + u];
+                        st_global_v8(dst + 32 * c + 16 * hh, w8);
                     }
-                }
-            }
-            // again, by the whole warp and from the row's own keys (each half
-            // stores its columns)
-            unsigned redo = __ballot_sync(0xffffffffu, live_row && !clean);
-            while (redo) {
-                const int who = __ffs(redo) - 1;
-                redo &= redo - 1;
-                const int R2 = it.row0 + X * kRows + 32 * wq + who, t2 = R2 / g;
-                const int pos2 = it.n - it.qlen + t2, head2 = it.h * g + R2 - t2 * g;
-                const int klo = max(first_key(md, it.s, pos2), it.b0 * PKV_BLOCK_SIZE);
-                const int khi = min(end_key(md, it.s, pos2, it.n),
-                                    (it.b0 + it.nblk) * PKV_BLOCK_SIZE);
-                float o2[D / 32], m2, l2;
-                plain_row<T, D>(p, it.s, it.h, head2, it.q0 + t2, pos2, klo, khi, o2, m2, l2);
-                const size_t prow2 = prow - lane + who;
-                T* dst2 = static_cast<T*>(p.out) + ((size_t)(it.q0 + t2) * Hq + head2) * D;
-                const float inv2 = l2 != 0.f ? 1.f / l2 : 0.f;
-                if (lane / 16 == q) {
+                } else {
 #pragma unroll
-                    for (int e = 0; e < D / 32; e += 2) {
-                        const int d = lane * (D / 32) + e;
-                        if (split) {
-                            p.ws_o[prow2 * D + d] = o2[e];
-                            p.ws_o[prow2 * D + d + 1] = o2[e + 1];
-                        } else {
-                            *reinterpret_cast<uint32_t*>(dst2 + d) =
-                                E::pack(o2[e] * inv2, o2[e + 1] * inv2);
-                        }
-                    }
-                }
-                if (split && lane == 0 && q == 0) {
-                    p.ws_m[prow2] = m2;
-                    p.ws_l[prow2] = l2;
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(dst + 32 * c + 8 * e) =
+                            make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[X]);
+            // rows whose weights are finite but whose O is not (a value of V that
+            // may be hidden from the row): again, from the row's own keys.  A row
+            // with a NaN among its own scores is NaN, as it should be; a row that
+            // sees nothing (l = 0) becomes zeros.
+            const unsigned redo = __ballot_sync(0xffffffffu, live_row && zero != 0.f && l - l == 0.f);
+            if (redo)
+                redo_rows<T, D>(p, it, it.row0 + X * kRows + 32 * wq, q, redo, l, prow - lane);
         }
     }
     tc_fence_before();
@@ -972,8 +1010,9 @@ Workspace ws_layout(long long rows, int head_dim) {
 template <int D>
 size_t prefill_smem() {
     // 2 Q tiles, 2 K and 2 V stages, barriers (under 1 KB) and the halves'
-    // maxima and sums (4 KB each); 1 KB alignment slack
-    return 1024 + (size_t)6 * (D / 64) * kRows * 128 + 1024 + 2 * 2 * 2 * 2 * kRows * 4;
+    // maxima and sums (4 KB each), the items; 1 KB alignment slack
+    return 1024 + (size_t)6 * (D / 64) * kRows * 128 + 1024 + 2 * 2 * 2 * 2 * kRows * 4 +
+           kItemCache * sizeof(Item);
 }
 
 template <typename T, int D, bool kCap, bool kBias, bool kFixed = false>
@@ -1010,7 +1049,7 @@ pkv_status launch_mods(const PrefillScored& prm, pkv_dtype dtype, int items, int
     if (!q_tma) tmq = tmk;  // unused
     const bool cap = prm.mods.cap_out > 0.f, bias = prm.mods.slopes != nullptr;
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        if (cap && !bias && prm.mods.cap_out <= kFixedMax)
+        if (cap && !bias && prm.mods.cap_out <= kFixedMax && prm.splits == 1)
             return launch<T, D, true, false, true>(prm, tmk, tmv, tmq, q_tma, items, ctas, stream);
     }
     if (cap)
