@@ -81,7 +81,7 @@ struct PrefillScored {
     int pairs_per_seq;     // ceil(max_q_len * group / kPair)
     int splits;            // key runs per item; > 1: partials go to the workspace
     float tanh_z[kTanhTerms];  // the polynomial's terms: z = raw sum tanh_z[i] raw^2i
-    float tanh_limit;      // largest (raw score)^2 it serves (negative: none)
+    float tanh_limit;      // largest |raw score| it serves (negative: none)
     // partials of split items: row = ((base item) * splits + split) * kPair + row of the pair
     float* ws_m;
     float* ws_l;
@@ -284,7 +284,7 @@ __device__ void plain_row(const PrefillScored& p, int s, int h, int head, int ro
 // O met something not finite; l: the lane's row's sum, which their partials are
 // relative to.
 template <typename T, int D>
-__device__ __noinline__ void redo_rows(const PrefillScored& p, const Item& it, int row0, int q,
+__device__ __noinline__ void redo_rows(const PrefillScored& p, Item it, int row0, int q,
                                        unsigned which, float l, size_t prow0) {
     const int lane = threadIdx.x & 31, g = p.group;
     while (which) {
@@ -310,43 +310,40 @@ __device__ __noinline__ void redo_rows(const PrefillScored& p, const Item& it, i
     }
 }
 
-// 32 raw scores to capped base-2 scores z = cap' tanh(raw cap_in), cap' = cap
+// Raw scores to capped base-2 scores z = cap' tanh(raw cap_in), cap' = cap
 // log2(e).  Where the whole warp's scores allow it z is raw times a polynomial
 // in raw^2, two scores an instruction; else cap' - 2 cap' / (1 + e^2x).
-__device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[32]) {
-    uint64_t v[16];
-    float top[2] = {0.f, 0.f};
+__device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[kHalf]) {
+    float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const uint64_t x = f2(sc[2 * e], sc[2 * e + 1]);
-        v[e] = f2_mul(x, x);
-        float a0, a1;
-        f2_split(v[e], a0, a1);
-        top[e & 1] = max3(top[e & 1], a0, a1);
-    }
-    if (__all_sync(0xffffffffu, fmaxf(top[0], top[1]) <= p.tanh_limit)) {
+    for (int c = 0; c < kHalf; c += 2)
+        top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], fabsf(sc[c]), fabsf(sc[c + 1]));
+    if (__all_sync(0xffffffffu, max3(fmaxf(top[0], top[1]), top[2], top[3]) <= p.tanh_limit)) {
         const uint64_t c3 = f2(p.tanh_z[3], p.tanh_z[3]), c2 = f2(p.tanh_z[2], p.tanh_z[2]);
         const uint64_t c1 = f2(p.tanh_z[1], p.tanh_z[1]), c0 = f2(p.tanh_z[0], p.tanh_z[0]);
 #pragma unroll
-        for (int e0 = 0; e0 < 16; e0 += 4) {  // four independent chains at a time
-            uint64_t y[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = f2_fma(c3, v[e0 + u], c2);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[e0 + u], c1);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[e0 + u], c0);
+        for (int e0 = 0; e0 < kHalf; e0 += 8) {  // four independent chains at a time
+            uint64_t x[4], v[4], y[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int e = e0 + u;
-                f2_split(f2_mul(f2(sc[2 * e], sc[2 * e + 1]), y[u]), sc[2 * e], sc[2 * e + 1]);
+                x[u] = f2(sc[e0 + 2 * u], sc[e0 + 2 * u + 1]);
+                v[u] = f2_mul(x[u], x[u]);
             }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = f2_fma(c3, v[u], c2);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[u], c1);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[u], c0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                f2_split(f2_mul(x[u], y[u]), sc[e0 + 2 * u], sc[e0 + 2 * u + 1]);
         }
     } else {
         const float k2 = 2.f * kScoreLog2e * p.mods.cap_in;
         const float cap = p.mods.cap_out;
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
+        for (int c = 0; c < kHalf; ++c)
             sc[c] = fmaf(-2.f * cap, fast_rcp(1.f + fast_exp2(k2 * sc[c])), cap);
     }
 }
@@ -380,8 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* o_free = bars + 20;           // [tile]: its score warps read O_X
     uint64_t* mma_idle = bars + 22;
     uint64_t* x_max = bars + 23;            // [tile][lane quarter]: both halves' maxima written
-    uint64_t* x_sum = bars + 31;            // [tile][lane quarter]: both halves' sums written
-    int* vbad = reinterpret_cast<int*>(bars + 39);           // [2] bad-block bits per V stage
+    uint64_t* x_scale = bars + 31;          // [tile][lane quarter]: both halves rescaled O
+    uint64_t* x_sum = bars + 39;            // [tile][lane quarter]: both halves' sums written
+    int* vbad = reinterpret_cast<int*>(bars + 47);           // [2] bad-block bits per V stage
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vbad + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     // what the two key halves of a row tell each other, by parity:
@@ -410,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&x_max[i], 2);
+            mbar_init(&x_scale[i], 2);
             mbar_init(&x_sum[i], 2);
         }
         mbar_init(mma_idle, 1);
@@ -652,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         int J = 0;             // key tiles of the CTA (the rings' count)
         int items = 0, tiles = 0;  // items and key tiles of this tile X
+        int rescales = 0;          // of this warp's rows
         bool ok = true;
         for (int rd = 0; rd < rounds && ok; ++rd) {
             Item it;
@@ -671,12 +671,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_used = kFixed ? 0.f : -INFINITY, l = 0.f;
             for (int j = 0; j < it.nkv; ++j, ++J, ++tiles) {
                 const int b = J & 1;
-                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[X], tiles & 1, abort_flag, p.status));
+                // V(J) first, as it is there long before the scores.  Not for an
+                // item's first tile: tile B's warps may come from far behind (items
+                // without a tile B), where the parity alone would not tell V(J)
+                // from V(J-4); S(J) written means that V(J-2) has been used.
+                if (j == 0)
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&s_full[X], tiles & 1, abort_flag, p.status));
                 if (!ok) break;
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(&v_full[b], (J >> 1) & 1, abort_flag, p.status));
                 if (!ok) break;
-                tc_fence_after();
                 const unsigned bad = ((unsigned)vbad[b] >> (4 * q)) & 0xFu;  // this half's blocks
                 const int key0 = it.b0 * PKV_BLOCK_SIZE + kKeys * j + kHalf * q;
                 const bool whole = bad == 0u && __all_sync(0xffffffffu, key0 >= lo &&
@@ -691,76 +696,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if ((bad >> (2 * w + 1)) & 1u) see &= 0x0000ffffu;
                     return see;
                 };
+                if (j > 0)
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&s_full[X], tiles & 1, abort_flag, p.status));
+                if (!ok) break;
+                tc_fence_after();
+                float sc[kHalf];
+                tc_ld32(sx, reinterpret_cast<uint32_t(&)[32]>(sc[0]));
+                tc_ld32(sx + 32, reinterpret_cast<uint32_t(&)[32]>(sc[32]));
+                tc_wait_ld();
                 uint64_t acc2[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
                 float f = 1.f;  // factor on what the row has so far
-                if constexpr (kFixed) {
-                    // |z| <= cap' <= kFixedMax: weights 2^z fit bf16 and their sums
-                    // fp32 without a maximum taken out
-#pragma unroll 1
+                // sc becomes z / mul (z: base-2 scores), with mul > 0
+                float mul = md.scale_log2, ms = 0.f;
+                if constexpr (kCap) {
+                    cap_to_z(p, sc);
+                    mul = 1.f;
+                }
+                if constexpr (kBias) {
+                    // distance |p - t|: keys before the row's position for all but
+                    // the tiles at the diagonal or in a prefix
+                    const uint64_t mul2 = f2(mul, mul);
+                    if (__all_sync(0xffffffffu, key0 + kHalf - 1 <= pos)) {
+                        const float base = slope2 * (float)(key0 - pos);
+#pragma unroll
+                        for (int c = 0; c < kHalf; c += 2) {
+                            const uint64_t bb = f2(fmaf(slope2, (float)c, base),
+                                                   fmaf(slope2, (float)(c + 1), base));
+                            f2_split(f2_fma(f2(sc[c], sc[c + 1]), mul2, bb), sc[c], sc[c + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kHalf; ++c)
+                            sc[c] = fmaf(-slope2, fabsf((float)(key0 + c - pos)), sc[c] * mul);
+                    }
+                    mul = 1.f;
+                } else if (mul <= 0.f) {
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c) sc[c] *= mul;
+                    mul = 1.f;
+                }
+                if (!whole) {  // select: hidden scores may be anything
+#pragma unroll
                     for (int w = 0; w < kHalf / 32; ++w) {
-                        float sc[32];
-                        tc_ld32(sx + 32 * w, reinterpret_cast<uint32_t(&)[32]>(sc));
-                        tc_wait_ld();
-                        cap_to_z(p, sc);
-                        if (!whole) {
-                            const uint32_t see = seen(w);
+                        const uint32_t see = seen(w);
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                sc[c] = (see >> c) & 1u ? sc[c] : -INFINITY;
-                        }
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float p0 = fast_exp2(sc[2 * e]), p1 = fast_exp2(sc[2 * e + 1]);
-                            acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
-                            pk[e] = E::pack(p0, p1);
-                        }
-                        tc_st16(sx + 16 * w, pk);
+                        for (int c = 0; c < 32; ++c)
+                            sc[32 * w + c] = (see >> c) & 1u ? sc[32 * w + c] : -INFINITY;
                     }
-                } else {
-                    float sc[kHalf];
-                    tc_ld32(sx, reinterpret_cast<uint32_t(&)[32]>(sc[0]));
-                    tc_ld32(sx + 32, reinterpret_cast<uint32_t(&)[32]>(sc[32]));
-                    tc_wait_ld();
-                    // sc becomes z / mul (z: base-2 scores), with mul > 0
-                    float mul = md.scale_log2;
-                    if constexpr (kCap) {
-                        cap_to_z(p, reinterpret_cast<float(&)[32]>(sc[0]));
-                        cap_to_z(p, reinterpret_cast<float(&)[32]>(sc[32]));
-                        mul = 1.f;
-                    }
-                    if constexpr (kBias) {
-                        // distance |p - t|: keys before the row's position for all but
-                        // the tiles at the diagonal or in a prefix
-                        const uint64_t mul2 = f2(mul, mul);
-                        if (__all_sync(0xffffffffu, key0 + kHalf - 1 <= pos)) {
-                            const float base = slope2 * (float)(key0 - pos);
-#pragma unroll
-                            for (int c = 0; c < kHalf; c += 2) {
-                                const uint64_t bb = f2(fmaf(slope2, (float)c, base),
-                                                       fmaf(slope2, (float)(c + 1), base));
-                                f2_split(f2_fma(f2(sc[c], sc[c + 1]), mul2, bb), sc[c], sc[c + 1]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < kHalf; ++c)
-                                sc[c] = fmaf(-slope2, fabsf((float)(key0 + c - pos)), sc[c] * mul);
-                        }
-                        mul = 1.f;
-                    } else if (mul <= 0.f) {
-#pragma unroll
-                        for (int c = 0; c < kHalf; ++c) sc[c] *= mul;
-                        mul = 1.f;
-                    }
-                    if (!whole) {  // select: hidden scores may be anything
-#pragma unroll
-                        for (int w = 0; w < kHalf / 32; ++w) {
-                            const uint32_t see = seen(w);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                sc[32 * w + c] = (see >> c) & 1u ? sc[32 * w + c] : -INFINITY;
-                        }
-                    }
+                }
+                // |z| <= cap' <= kFixedMax (kFixed): weights 2^z fit bf16 and their
+                // sums fp32 without a maximum taken out
+                if constexpr (!kFixed) {
                     float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < kHalf; c += 2)
@@ -780,8 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool grow = m_used != -INFINITY && m_new > m_used + kRescale;
                     f = grow ? fast_exp2(m_used - m_new) : 1.f;
                     if (m_used == -INFINITY || grow) m_used = m_new;
-                    const float ms = m_used == -INFINITY ? 0.f : m_used;
-                    if (__any_sync(0xffffffffu, grow)) {
+                    ms = m_used == -INFINITY ? 0.f : m_used;
+                    if (__any_sync(0xffffffffu, grow)) {  // (the same in both halves' warps)
                         // S_X(J) was issued after P V_X(J-1): O_X holds every earlier tile
 #pragma unroll 1
                         for (int c = 0; c < D / 64; ++c) {
@@ -793,35 +780,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                             tc_st32(ox + 32 * c, o);
                         }
-                    }
-                    // P as 16-bit pairs (every score is in registers); the sum takes
-                    // the unrounded weights
-                    const uint64_t mul2 = f2(mul, mul), nms2 = f2(-ms, -ms);
-#pragma unroll
-                    for (int w = 0; w < kHalf / 32; ++w) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float a0, a1;
-                            f2_split(f2_fma(f2(sc[32 * w + 2 * e], sc[32 * w + 2 * e + 1]), mul2,
-                                            nms2),
-                                     a0, a1);
-                            const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-                            acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
-                            pk[e] = E::pack(p0, p1);
-                        }
-                        tc_st16(sx + 16 * w, pk);
+                        // P V of either key half adds to every column of O: neither
+                        // half lets its P go before both have rescaled their columns
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&x_scale[4 * X + wq]);
+                        ok = __all_sync(0xffffffffu, mbar_wait(&x_scale[4 * X + wq], rescales & 1,
+                                                               abort_flag, p.status));
+                        if (!ok) break;
+                        ++rescales;
                     }
                 }
-                float psum = 0.f;
+                // P as 16-bit pairs (every score is in registers); the sum takes
+                // the unrounded weights
+                const uint64_t mul2 = f2(mul, mul), nms2 = f2(-ms, -ms);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float a0, a1;
-                    f2_split(acc2[e], a0, a1);
-                    psum += a0 + a1;
+                for (int w = 0; w < kHalf / 32; ++w) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float a0 = sc[32 * w + 2 * e], a1 = sc[32 * w + 2 * e + 1];
+                        if constexpr (!kFixed) f2_split(f2_fma(f2(a0, a1), mul2, nms2), a0, a1);
+                        const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                        acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
+                        pk[e] = E::pack(p0, p1);
+                    }
+                    tc_st16(sx + 16 * w, pk);
                 }
                 tc_wait_st();
-                l = l * f + psum;
                 // V rows that no row of the item sees (or that were not loaded)
                 // become zeros before P V; both tiles zero the same rows
                 if (j == 0 || j == it.nkv - 1 || bad) {
@@ -838,6 +825,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();  // P and a rescaled O are ordered before the next MMA
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[2 * X + q]);
+                float psum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float a0, a1;
+                    f2_split(acc2[e], a0, a1);
+                    psum += a0 + a1;
+                }
+                l = l * f + psum;
             }
             if (!ok) break;
             // ---- epilogue: O_X / l (this half's columns) for the rows of the chunk,
@@ -1143,8 +1138,8 @@ pkv_status paged_attention_prefill_scored(
             prm.tanh_z[i] = (float)(pkv::tanh_term(i) * f * prm.mods.scale_log2);
             ok = ok && std::isnormal(prm.tanh_z[i]);
         }
-        const double limit = pkv::kTanhRange * pkv::kTanhRange / c2;
-        if (ok && std::isnormal((float)limit)) prm.tanh_limit = (float)limit;
+        const float limit = pkv::kTanhRange / std::fabs(prm.mods.cap_in);
+        if (ok && limit < 1e18f) prm.tanh_limit = limit;  // (its square is finite)
     }
     const pkv::Workspace ws =
         pkv::ws_layout(pl.splits > 1 ? pl.items * pl.splits * pkv::kPair : 0, head_dim);
