@@ -221,6 +221,40 @@ __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&w)[8]) 
                  : "memory");
 }
 
+// One lane of a converged warp (1 there, 0 elsewhere).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(one));
+    return one;
+}
+// tc_mma, tc_mma_tmem_a and tc_commit by the elected lane of a whole warp.
+__device__ __forceinline__ void mma_if(uint32_t leader, uint32_t d_tmem, uint64_t a_desc,
+                                       uint64_t b_desc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_tmem_a_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                              uint64_t b_desc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+            smem_addr(bar)),
+        "r"(leader)
+        : "memory");
+}
+
 // One row again, by a whole warp and from its own keys only (keys [lo, hi) of
 // its sequence): a key it does not see, or whose block id is bad, is never
 // read.  Lane x gets elements x * D / 32 .. of the (normalised) output.
@@ -389,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item* table = reinterpret_cast<Item*>(
         (reinterpret_cast<uintptr_t>(xl + 2 * 2 * 2 * kRows) + 15) & ~(uintptr_t)15);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one per warp
     const int g = p.group, Hq = p.num_q_heads;
 
     if (tid == 0) {
@@ -538,103 +573,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-            const uint32_t id_s = tc_idesc_f16(kBf16, kRows, kKeys, 0, 0);
-            const uint32_t id_pv = tc_idesc_f16(kBf16, kRows, D, 0, 1);
-            const uint32_t aq = smem_addr(sq), ak = smem_addr(sk), av = smem_addr(sv);
-            // a cursor over the key tiles of this CTA's items, in order; per
-            // tile X the items and key tiles it took part in
-            struct Cur {
-                int r, j, J, nkv;
-                int items[2], tiles[2];
-                bool has_b;
-            };
-            auto advance = [&](Cur& c) -> bool {
-                if (c.r >= 0 && ++c.j < c.nkv) {
-                    ++c.J;
-                    ++c.tiles[0];
-                    if (c.has_b) ++c.tiles[1];
-                    return true;
-                }
-                for (++c.r; c.r < rounds; ++c.r) {
-                    Item it;
-                    if (!round_at(p, table, num_items, c.r, false, it) || it.nkv == 0) continue;
-                    c.nkv = it.nkv;
-                    c.has_b = it.has_b;
-                    c.j = 0;
-                    ++c.J;
-                    ++c.items[0];
-                    ++c.tiles[0];
-                    if (c.has_b) {
-                        ++c.items[1];
-                        ++c.tiles[1];
-                    }
-                    return true;
-                }
-                return false;
-            };
-            // S_X(c) = Q_X K(c)^T into tile X's score buffer, over the last
-            // P_X, whose P V this thread issued before (MMAs run in order)
-            auto issue_s = [&](const Cur& c, int X) -> bool {
-                const int b = c.J & 1;
-                if (X == 0 && !mbar_wait(&k_full[b], (c.J >> 1) & 1, abort_flag, p.status))
-                    return false;
-                if (c.j == 0 && !mbar_wait(&q_full[X], c.items[X] & 1, abort_flag, p.status))
-                    return false;
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc_mma(tmem + X * kKeys,
-                           tc_smem_desc(aq + X * TILE + (ks >> 2) * REG + (ks & 3) * 32, 16, 1024),
-                           tc_smem_desc(ak + b * TILE + (ks >> 2) * REG + (ks & 3) * 32, 16, 1024),
-                           id_s, ks > 0);
-                tc_commit(&s_full[X]);
-                if (X == 1 || !c.has_b) tc_commit(&k_empty[b]);
-                if (c.j == c.nkv - 1) tc_commit(&q_empty[X]);
+        // The whole warp walks the loop and one elected lane issues: descriptors,
+        // addresses and conditions are then the same in all lanes and live in
+        // uniform registers, which is where the MMA instruction takes them from.
+        constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+        const uint32_t leader = elect_one();
+        const uint32_t id_s = tc_idesc_f16(kBf16, kRows, kKeys, 0, 0);
+        const uint32_t id_pv = tc_idesc_f16(kBf16, kRows, D, 0, 1);
+        // operand descriptors: a step of x bytes adds x / 16 to the address field
+        const uint64_t dq = tc_smem_desc(smem_addr(sq), 16, 1024);
+        const uint64_t dk = tc_smem_desc(smem_addr(sk), 16, 1024);
+        const uint64_t dv = tc_smem_desc(smem_addr(sv), REG, 1024);
+        auto wait = [&](uint64_t* bar, int parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status));
+        };
+        // a cursor over the key tiles of this CTA's items, in order; per
+        // tile X the items and key tiles it took part in
+        struct Cur {
+            int r, j, J, nkv, has_b;
+            int items[2], tiles[2];
+        };
+        auto advance = [&](Cur& c) -> bool {
+            if (c.r >= 0 && ++c.j < c.nkv) {
+                ++c.J;
+                ++c.tiles[0];
+                if (c.has_b) ++c.tiles[1];
                 return true;
-            };
-            // O_X += P_X(c) V(c): the P of a key half over the first 32 columns
-            // of that half's scores
-            auto issue_pv = [&](const Cur& c, int X) -> bool {
-                const int b = c.J & 1;
-                if (X == 0 && !mbar_wait(&v_full[b], (c.J >> 1) & 1, abort_flag, p.status))
-                    return false;
-                // the item's first P V overwrites O_X: the last item's must have been read
-                if (c.j == 0 && c.items[X] >= 1 &&
-                    !mbar_wait(&o_free[X], (c.items[X] - 1) & 1, abort_flag, p.status))
-                    return false;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (!mbar_wait(&p_full[2 * X + q], c.tiles[X] & 1, abort_flag, p.status))
-                        return false;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < kHalf / 16; ++kk)
-                        tc_mma_tmem_a(tmem + kOCol + X * D, tmem + X * kKeys + kHalf * q + 8 * kk,
-                                      tc_smem_desc(av + b * TILE + (q * (kHalf / 16) + kk) * 2048,
-                                                   REG, 1024),
-                                      id_pv, c.j > 0 || q > 0 || kk > 0);
-                }
-                if (X == 1 || !c.has_b) tc_commit(&v_empty[b]);
-                if (c.j == c.nkv - 1) tc_commit(&o_ready[X]);
-                return true;
-            };
-            Cur cs = {-1, 0, -1, 0, {-1, -1}, {-1, -1}, false}, cp = cs;
-            bool live = true;
-            bool more = advance(cs);
-            if (more) live = issue_s(cs, 0) && (!cs.has_b || issue_s(cs, 1));
-            while (live && advance(cp)) {
-                more = advance(cs);
-                live = issue_pv(cp, 0);
-                if (live && more) live = issue_s(cs, 0);
-                if (live && cp.has_b) live = issue_pv(cp, 1);
-                if (live && more && cs.has_b) live = issue_s(cs, 1);
             }
-            // nothing of this thread's may still run when tensor memory is freed
-            tc_commit(mma_idle);
-            mbar_drain(mma_idle, 0, p.status);
+            for (++c.r; c.r < rounds; ++c.r) {
+                Item it;
+                const bool any = round_at(p, table, num_items, c.r, false, it);
+                c.nkv = __shfl_sync(0xffffffffu, any ? it.nkv : 0, 0);
+                c.has_b = __shfl_sync(0xffffffffu, it.has_b, 0);
+                if (c.nkv == 0) continue;
+                c.j = 0;
+                ++c.J;
+                ++c.items[0];
+                ++c.tiles[0];
+                if (c.has_b) {
+                    ++c.items[1];
+                    ++c.tiles[1];
+                }
+                return true;
+            }
+            return false;
+        };
+        // S_X(c) = Q_X K(c)^T into tile X's score buffer, over the last P_X, whose
+        // P V was issued before (MMAs run in order)
+        auto issue_s = [&](const Cur& c, int X) -> bool {
+            const int b = c.J & 1;
+            if (X == 0 && !wait(&k_full[b], (c.J >> 1) & 1)) return false;
+            if (c.j == 0 && !wait(&q_full[X], c.items[X] & 1)) return false;
+            tc_fence_after();
+            const uint64_t da = dq + X * (TILE / 16), db = dk + b * (TILE / 16);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_if(leader, tmem + X * kKeys, da + ((ks >> 2) * REG + (ks & 3) * 32) / 16,
+                       db + ((ks >> 2) * REG + (ks & 3) * 32) / 16, id_s, ks > 0);
+            commit_if(leader, &s_full[X]);
+            if (X == 1 || !c.has_b) commit_if(leader, &k_empty[b]);
+            if (c.j == c.nkv - 1) commit_if(leader, &q_empty[X]);
+            return true;
+        };
+        // O_X += P_X(c) V(c): the P of a key half over the first 32 columns of that
+        // half's scores
+        auto issue_pv = [&](const Cur& c, int X) -> bool {
+            const int b = c.J & 1;
+            if (X == 0 && !wait(&v_full[b], (c.J >> 1) & 1)) return false;
+            // the item's first P V overwrites O_X: the last item's must have been read
+            if (c.j == 0 && c.items[X] >= 1 && !wait(&o_free[X], (c.items[X] - 1) & 1))
+                return false;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (!wait(&p_full[2 * X + q], c.tiles[X] & 1)) return false;
+                tc_fence_after();
+                const uint64_t db = dv + b * (TILE / 16) + q * (kHalf / 16) * 128;
+#pragma unroll
+                for (int kk = 0; kk < kHalf / 16; ++kk)
+                    mma_tmem_a_if(leader, tmem + kOCol + X * D,
+                                  tmem + X * kKeys + kHalf * q + 8 * kk, db + kk * 128, id_pv,
+                                  c.j > 0 || q > 0 || kk > 0);
+            }
+            if (X == 1 || !c.has_b) commit_if(leader, &v_empty[b]);
+            if (c.j == c.nkv - 1) commit_if(leader, &o_ready[X]);
+            return true;
+        };
+        Cur cs = {-1, 0, -1, 0, 0, {-1, -1}, {-1, -1}}, cp = cs;
+        bool live = true;
+        bool more = advance(cs);
+        if (more) live = issue_s(cs, 0) && (!cs.has_b || issue_s(cs, 1));
+        while (live && advance(cp)) {
+            more = advance(cs);
+            live = issue_pv(cp, 0);
+            if (live && more) live = issue_s(cs, 0);
+            if (live && cp.has_b) live = issue_pv(cp, 1);
+            if (live && more && cs.has_b) live = issue_s(cs, 1);
         }
+        // nothing of the leader's may still run when tensor memory is freed
+        commit_if(leader, mma_idle);
+        mbar_drain(mma_idle, 0, p.status);
         __syncwarp();
     }
     } else {
