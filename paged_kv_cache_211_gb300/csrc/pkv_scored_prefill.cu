@@ -58,13 +58,13 @@ static_assert(128 * kOtherRegs + kSoftWarps * 32 * kSoftmaxRegs <= kThreads * kL
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// tanh(x) / x on |x| <= 0.5 as a polynomial in x^2: fitted here by iterated
-// weighted least squares to the smallest largest relative error, 5.5e-7.
-constexpr float kTanhRange = 0.5f;
-constexpr int kTanhTerms = 4;
-__host__ __device__ constexpr float tanh_term(int i) {
-    return i == 0 ? 0.999999456f : i == 1 ? -0.333263179f : i == 2 ? 0.131902966f : -0.0444022261f;
-}
+// tanh(x) / x as polynomials in x^2, fitted here by iterated weighted least
+// squares to the smallest largest relative error: four terms for |x| <= 0.5
+// (5.5e-7) and three for |x| <= 0.25 (4.0e-7).
+constexpr int kTanhTerms = 4, kTanhFew = 3;
+constexpr float kTanhRange = 0.5f, kTanhFewRange = 0.25f;
+constexpr float kTanh[kTanhTerms] = {0.999999456f, -0.333263179f, 0.131902966f, -0.0444022261f};
+constexpr float kTanhS[kTanhFew] = {0.999999604f, -0.333219082f, 0.128416134f};
 
 struct PrefillScored {
     const void* q;
@@ -80,8 +80,10 @@ struct PrefillScored {
     int max_q_len, num_q_rows;
     int pairs_per_seq;     // ceil(max_q_len * group / kPair)
     int splits;            // key runs per item; > 1: partials go to the workspace
-    float tanh_z[kTanhTerms];  // the polynomial's terms: z = raw sum tanh_z[i] raw^2i
-    float tanh_limit;      // largest |raw score| it serves (negative: none)
+    // the polynomials' terms, z = raw sum tanh_z[i] raw^2i, and the largest |raw
+    // score| that each serves (negative: none)
+    float tanh_z[kTanhTerms], tanh_few[kTanhFew];
+    float tanh_limit, tanh_few_limit;
     // partials of split items: row = ((base item) * splits + split) * kPair + row of the pair
     float* ws_m;
     float* ws_l;
@@ -347,12 +349,16 @@ __device__ __noinline__ void redo_rows(const PrefillScored& p, Item it, int row0
 // Raw scores to capped base-2 scores z = cap' tanh(raw cap_in), cap' = cap
 // log2(e).  Where the whole warp's scores allow it z is raw times a polynomial
 // in raw^2, two scores an instruction; else cap' - 2 cap' / (1 + e^2x).
-__device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[kHalf]) {
+// top: the largest |raw score|.
+__device__ __forceinline__ float largest(const float (&sc)[kHalf]) {
     float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < kHalf; c += 2)
         top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], fabsf(sc[c]), fabsf(sc[c + 1]));
-    if (__all_sync(0xffffffffu, max3(fmaxf(top[0], top[1]), top[2], top[3]) <= p.tanh_limit)) {
+    return max3(fmaxf(top[0], top[1]), top[2], top[3]);
+}
+__device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[kHalf], float top) {
+    if (__all_sync(0xffffffffu, top <= p.tanh_limit)) {
         const uint64_t c3 = f2(p.tanh_z[3], p.tanh_z[3]), c2 = f2(p.tanh_z[2], p.tanh_z[2]);
         const uint64_t c1 = f2(p.tanh_z[1], p.tanh_z[1]), c0 = f2(p.tanh_z[0], p.tanh_z[0]);
 #pragma unroll
@@ -746,109 +752,149 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float f = 1.f;  // factor on what the row has so far
                 // sc becomes z / mul (z: base-2 scores), with mul > 0
                 float mul = md.scale_log2, ms = 0.f;
+                bool done = false;
                 if constexpr (kCap) {
-                    cap_to_z(p, sc);
+                    const float top = largest(sc);
                     mul = 1.f;
-                }
-                if constexpr (kBias) {
-                    // distance |p - t|: keys before the row's position for all but
-                    // the tiles at the diagonal or in a prefix
-                    const uint64_t mul2 = f2(mul, mul);
-                    if (__all_sync(0xffffffffu, key0 + kHalf - 1 <= pos)) {
-                        const float base = slope2 * (float)(key0 - pos);
+                    if (kFixed && whole && __all_sync(0xffffffffu, top <= p.tanh_few_limit)) {
+                        // the common case in one piece, so that polynomials (fp32
+                        // pipe) and exponentials (special-function pipe) overlap
+                        const uint64_t c2 = f2(p.tanh_few[2], p.tanh_few[2]);
+                        const uint64_t c1 = f2(p.tanh_few[1], p.tanh_few[1]);
+                        const uint64_t c0 = f2(p.tanh_few[0], p.tanh_few[0]);
 #pragma unroll
-                        for (int c = 0; c < kHalf; c += 2) {
-                            const uint64_t bb = f2(fmaf(slope2, (float)c, base),
-                                                   fmaf(slope2, (float)(c + 1), base));
-                            f2_split(f2_fma(f2(sc[c], sc[c + 1]), mul2, bb), sc[c], sc[c + 1]);
+                        for (int w = 0; w < kHalf / 32; ++w) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e0 = 0; e0 < 16; e0 += 4) {
+                                uint64_t x[4], v[4], y[4];
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    const int c = 32 * w + 2 * (e0 + u);
+                                    x[u] = f2(sc[c], sc[c + 1]);
+                                    v[u] = f2_mul(x[u], x[u]);
+                                }
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) y[u] = f2_fma(c2, v[u], c1);
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[u], c0);
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    float a0, a1;
+                                    f2_split(f2_mul(x[u], y[u]), a0, a1);
+                                    const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                                    acc2[u] = f2_add(acc2[u], f2(p0, p1));
+                                    pk[e0 + u] = E::pack(p0, p1);
+                                }
+                            }
+                            tc_st16(sx + 16 * w, pk);
                         }
+                        done = true;
                     } else {
-#pragma unroll
-                        for (int c = 0; c < kHalf; ++c)
-                            sc[c] = fmaf(-slope2, fabsf((float)(key0 + c - pos)), sc[c] * mul);
-                    }
-                    mul = 1.f;
-                } else if (mul <= 0.f) {
-#pragma unroll
-                    for (int c = 0; c < kHalf; ++c) sc[c] *= mul;
-                    mul = 1.f;
-                }
-                if (!whole) {  // select: hidden scores may be anything
-#pragma unroll
-                    for (int w = 0; w < kHalf / 32; ++w) {
-                        const uint32_t see = seen(w);
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            sc[32 * w + c] = (see >> c) & 1u ? sc[32 * w + c] : -INFINITY;
+                        cap_to_z(p, sc, top);
                     }
                 }
-                // |z| <= cap' <= kFixedMax (kFixed): weights 2^z fit bf16 and their
-                // sums fp32 without a maximum taken out
-                if constexpr (!kFixed) {
-                    float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (!done) {
+                    if constexpr (kBias) {
+                        // distance |p - t|: keys before the row's position for all but
+                        // the tiles at the diagonal or in a prefix
+                        const uint64_t mul2 = f2(mul, mul);
+                        if (__all_sync(0xffffffffu, key0 + kHalf - 1 <= pos)) {
+                            const float base = slope2 * (float)(key0 - pos);
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 2)
-                        mxp[(c >> 1) & 3] = max3(mxp[(c >> 1) & 3], sc[c], sc[c + 1]);
-                    float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mul;
-                    // the row's maximum over both halves
-                    float* mine = xm + (((tiles & 1) * 2 + X) * 2 + q) * kRows + r;
-                    *mine = mx;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&x_max[4 * X + wq]);
-                    ok = __all_sync(0xffffffffu, mbar_wait(&x_max[4 * X + wq], tiles & 1,
-                                                           abort_flag, p.status));
-                    if (!ok) break;
-                    mx = fmaxf(mx, *(mine + (q ? -kRows : kRows)));
-                    const float m_new = fmaxf(m_used, mx);
-                    // lazy rescale: only when the maximum grew by more than 2^kRescale
-                    const bool grow = m_used != -INFINITY && m_new > m_used + kRescale;
-                    f = grow ? fast_exp2(m_used - m_new) : 1.f;
-                    if (m_used == -INFINITY || grow) m_used = m_new;
-                    ms = m_used == -INFINITY ? 0.f : m_used;
-                    if (__any_sync(0xffffffffu, grow)) {  // (the same in both halves' warps)
-                        // S_X(J) was issued after P V_X(J-1): O_X holds every earlier tile
-#pragma unroll 1
-                        for (int c = 0; c < D / 64; ++c) {
-                            uint32_t o[32];
-                            tc_ld32(ox + 32 * c, o);
-                            tc_wait_ld();
+                            for (int c = 0; c < kHalf; c += 2) {
+                                const uint64_t bb = f2(fmaf(slope2, (float)c, base),
+                                                       fmaf(slope2, (float)(c + 1), base));
+                                f2_split(f2_fma(f2(sc[c], sc[c + 1]), mul2, bb), sc[c], sc[c + 1]);
+                            }
+                        } else {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc_st32(ox + 32 * c, o);
+                            for (int c = 0; c < kHalf; ++c)
+                                sc[c] = fmaf(-slope2, fabsf((float)(key0 + c - pos)), sc[c] * mul);
                         }
-                        // P V of either key half adds to every column of O: neither
-                        // half lets its P go before both have rescaled their columns
-                        tc_wait_st();
-                        tc_fence_before();
+                        mul = 1.f;
+                    } else if (mul <= 0.f) {
+#pragma unroll
+                        for (int c = 0; c < kHalf; ++c) sc[c] *= mul;
+                        mul = 1.f;
+                    }
+                    if (!whole) {  // select: hidden scores may be anything
+#pragma unroll
+                        for (int w = 0; w < kHalf / 32; ++w) {
+                            const uint32_t see = seen(w);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                sc[32 * w + c] = (see >> c) & 1u ? sc[32 * w + c] : -INFINITY;
+                        }
+                    }
+                    // |z| <= cap' <= kFixedMax (kFixed): weights 2^z fit bf16 and their
+                    // sums fp32 without a maximum taken out
+                    if constexpr (!kFixed) {
+                        float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < kHalf; c += 2)
+                            mxp[(c >> 1) & 3] = max3(mxp[(c >> 1) & 3], sc[c], sc[c + 1]);
+                        float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mul;
+                        // the row's maximum over both halves
+                        float* mine = xm + (((tiles & 1) * 2 + X) * 2 + q) * kRows + r;
+                        *mine = mx;
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&x_scale[4 * X + wq]);
-                        ok = __all_sync(0xffffffffu, mbar_wait(&x_scale[4 * X + wq], rescales & 1,
+                        if (lane == 0) mbar_arrive(&x_max[4 * X + wq]);
+                        ok = __all_sync(0xffffffffu, mbar_wait(&x_max[4 * X + wq], tiles & 1,
                                                                abort_flag, p.status));
                         if (!ok) break;
-                        ++rescales;
-                    }
-                }
-                // P as 16-bit pairs (every score is in registers); the sum takes
-                // the unrounded weights
-                const uint64_t mul2 = f2(mul, mul), nms2 = f2(-ms, -ms);
+                        mx = fmaxf(mx, *(mine + (q ? -kRows : kRows)));
+                        const float m_new = fmaxf(m_used, mx);
+                        // lazy rescale: only when the maximum grew by more than 2^kRescale
+                        const bool grow = m_used != -INFINITY && m_new > m_used + kRescale;
+                        f = grow ? fast_exp2(m_used - m_new) : 1.f;
+                        if (m_used == -INFINITY || grow) m_used = m_new;
+                        ms = m_used == -INFINITY ? 0.f : m_used;
+                        if (__any_sync(0xffffffffu, grow)) {  // (the same in both halves' warps)
+                            // S_X(J) was issued after P V_X(J-1): O_X holds every earlier tile
+#pragma unroll 1
+                            for (int c = 0; c < D / 64; ++c) {
+                                uint32_t o[32];
+                                tc_ld32(ox + 32 * c, o);
+                                tc_wait_ld();
 #pragma unroll
-                for (int w = 0; w < kHalf / 32; ++w) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float a0 = sc[32 * w + 2 * e], a1 = sc[32 * w + 2 * e + 1];
-                        if constexpr (!kFixed) f2_split(f2_fma(f2(a0, a1), mul2, nms2), a0, a1);
-                        const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-                        acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
-                        pk[e] = E::pack(p0, p1);
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tc_st32(ox + 32 * c, o);
+                            }
+                            // P V of either key half adds to every column of O: neither
+                            // half lets its P go before both have rescaled their columns
+                            tc_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&x_scale[4 * X + wq]);
+                            ok = __all_sync(0xffffffffu, mbar_wait(&x_scale[4 * X + wq], rescales & 1,
+                                                                   abort_flag, p.status));
+                            if (!ok) break;
+                            ++rescales;
+                        }
                     }
-                    tc_st16(sx + 16 * w, pk);
+                    // P as 16-bit pairs (every score is in registers); the sum takes
+                    // the unrounded weights
+                    const uint64_t mul2 = f2(mul, mul), nms2 = f2(-ms, -ms);
+#pragma unroll
+                    for (int w = 0; w < kHalf / 32; ++w) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float a0 = sc[32 * w + 2 * e], a1 = sc[32 * w + 2 * e + 1];
+                            if constexpr (!kFixed) f2_split(f2_fma(f2(a0, a1), mul2, nms2), a0, a1);
+                            const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                            acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
+                            pk[e] = E::pack(p0, p1);
+                        }
+                        tc_st16(sx + 16 * w, pk);
+                    }
                 }
                 tc_wait_st();
                 // V rows that no row of the item sees (or that were not loaded)
                 // become zeros before P V; both tiles zero the same rows
-                if (j == 0 || j == it.nkv - 1 || bad) {
+                if (key0 < it.lo || key0 + kHalf > it.hi || bad) {
                     unsigned char* vt = sv + b * TILE + kHalf * q * 128;
                     for (int x = r; x < kHalf * 8 * HALVES; x += kRows) {
                         const int kq = x / (8 * HALVES), rest = x - kq * (8 * HALVES);
@@ -1166,17 +1212,21 @@ pkv_status paged_attention_prefill_scored(
     prm.pairs_per_seq = pl.pairs;
     prm.splits = pl.splits;
     // z = cap' x (tanh(x) / x) with x = raw cap_in: the terms in raw^2, times cap' cap_in
-    prm.tanh_limit = -1.f;
+    prm.tanh_limit = prm.tanh_few_limit = -1.f;
     if (softcap > 0.f && scale != 0.f) {
         const double c2 = (double)prm.mods.cap_in * prm.mods.cap_in;
-        double f = 1.0;
+        double f = prm.mods.scale_log2;
         bool ok = true;
         for (int i = 0; i < pkv::kTanhTerms; ++i, f *= c2) {
-            prm.tanh_z[i] = (float)(pkv::tanh_term(i) * f * prm.mods.scale_log2);
+            prm.tanh_z[i] = (float)(pkv::kTanh[i] * f);
             ok = ok && std::isnormal(prm.tanh_z[i]);
+            if (i < pkv::kTanhFew) prm.tanh_few[i] = (float)(pkv::kTanhS[i] * f);
         }
         const float limit = pkv::kTanhRange / std::fabs(prm.mods.cap_in);
-        if (ok && limit < 1e18f) prm.tanh_limit = limit;  // (its square is finite)
+        if (ok && limit < 1e18f) {  // (its square is finite)
+            prm.tanh_limit = limit;
+            prm.tanh_few_limit = pkv::kTanhFewRange / std::fabs(prm.mods.cap_in);
+        }
     }
     const pkv::Workspace ws =
         pkv::ws_layout(pl.splits > 1 ? pl.items * pl.splits * pkv::kPair : 0, head_dim);
