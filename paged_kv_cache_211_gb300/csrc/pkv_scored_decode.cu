@@ -540,11 +540,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of one row (sequence, head group).  The CTA of worker w acts
 // if w is the second worker of the row its run starts in; warp (e, i) has
 // fragment i of head e from every part.
+constexpr int kFewParts = 6;
+
 template <typename T, int D, int HPS>
 __global__ void __launch_bounds__(HPS * (D / 16) * 32)
     scored_join_kernel(const RowDesc* __restrict__ desc, const float2* __restrict__ ml,
                        const float4* __restrict__ o, void* out, int num_q_heads, int g) {
     constexpr int KS = D / 16;
+    // the next kernel's CTAs may be scheduled beside these; it waits for this
+    // grid before it touches anything (griddepcontrol.wait)
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const RowDesc d = desc[blockIdx.x];
     if (d.s < 0 || d.first + 1 != (int)blockIdx.x) return;
@@ -556,34 +561,51 @@ __global__ void __launch_bounds__(HPS * (D / 16) * 32)
         return *reinterpret_cast<const float4*>(ml + ((size_t)slot_of(c) * HPS + e) * kMaxGroup +
                                                 2 * tig);
     };
-    float M0 = -INFINITY, M1 = -INFINITY;
-    for (int c = d.first + gid; c <= d.last; c += 8) {
-        if (!has) break;
-        const float4 v = ml_of(c);
-        M0 = fmaxf(M0, v.x);
-        M1 = fmaxf(M1, v.z);
-    }
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-        M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, off));
-        M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, off));
-    }
-    if (M0 == -INFINITY) M0 = 0.f;
-    if (M1 == -INFINITY) M1 = 0.f;
-    float L0 = 0.f, L1 = 0.f;
+    auto o_of = [&](int c) { return o[(((size_t)slot_of(c) * HPS + e) * KS + i) * 32 + lane]; };
+    float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (has) {
-#pragma unroll 4
-        for (int c = d.first; c <= d.last; ++c) {
+    auto add = [&](const float4& v, const float4& x) {
+        const float w0 = fast_exp2(v.x - M0), w1 = fast_exp2(v.z - M1);
+        L0 += w0 * v.y;
+        L1 += w1 * v.w;
+        acc.x += w0 * x.x;
+        acc.y += w1 * x.y;
+        acc.z += w0 * x.z;
+        acc.w += w1 * x.w;
+    };
+    if (d.last - d.first < kFewParts) {  // (uniform) every load at once
+        float4 v[kFewParts], x[kFewParts];
+#pragma unroll
+        for (int k = 0; k < kFewParts; ++k) {
+            const bool here = has && d.first + k <= d.last;
+            v[k] = here ? ml_of(d.first + k) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+            x[k] = here ? o_of(d.first + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kFewParts; ++k) {
+            M0 = fmaxf(M0, v[k].x);
+            M1 = fmaxf(M1, v[k].z);
+        }
+        if (M0 == -INFINITY) M0 = 0.f;
+        if (M1 == -INFINITY) M1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < kFewParts; ++k) add(v[k], x[k]);
+    } else {
+        for (int c = d.first + gid; has && c <= d.last; c += 8) {
             const float4 v = ml_of(c);
-            const float4 x = o[(((size_t)slot_of(c) * HPS + e) * KS + i) * 32 + lane];
-            const float w0 = fast_exp2(v.x - M0), w1 = fast_exp2(v.z - M1);
-            L0 += w0 * v.y;
-            L1 += w1 * v.w;
-            acc.x += w0 * x.x;
-            acc.y += w1 * x.y;
-            acc.z += w0 * x.z;
-            acc.w += w1 * x.w;
+            M0 = fmaxf(M0, v.x);
+            M1 = fmaxf(M1, v.z);
+        }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, off));
+            M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, off));
+        }
+        if (M0 == -INFINITY) M0 = 0.f;
+        if (M1 == -INFINITY) M1 = 0.f;
+        if (has) {
+#pragma unroll 8
+            for (int c = d.first; c <= d.last; ++c) add(ml_of(c), o_of(c));
         }
     }
     const float inv0 = L0 != 0.f ? 1.f / L0 : 0.f, inv1 = L1 != 0.f ? 1.f / L1 : 0.f;
