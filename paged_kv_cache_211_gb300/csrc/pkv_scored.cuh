@@ -25,6 +25,30 @@ struct ScoreMods {
 
 constexpr float kScoreLog2e = 1.4426950408889634f;
 
+// tanh(x) / x as polynomials in x^2, fitted here by iterated weighted least
+// squares to the smallest largest relative error: four terms for |x| <= 0.5
+// (5.5e-7) and three for |x| <= 0.25 (4.0e-7).
+constexpr int kTanhTerms = 4, kTanhFew = 3;
+constexpr float kTanhRange = 0.5f, kTanhFewRange = 0.25f;
+constexpr float kTanh4[kTanhTerms] = {0.999999456f, -0.333263179f, 0.131902966f, -0.0444022261f};
+constexpr float kTanh3[kTanhFew] = {0.999999604f, -0.333219082f, 0.128416134f};
+
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The capped base-2 score of a raw one: cap' tanh(x), x = raw cap_in.  Away from
+// zero 1 - 2 / (1 + e^2x) from exp2 and a reciprocal (errors of 2^-22 of 1); near
+// it that would cancel, and the polynomial keeps the relative error.
+__device__ __forceinline__ float cap_score(float raw, const ScoreMods& m) {
+    const float x = raw * m.cap_in, v = x * x;
+    const float far = fmaf(-2.f, fast_rcp(1.f + fast_exp2(2.f * kScoreLog2e * x)), 1.f);
+    const float near = x * fmaf(fmaf(kTanh3[2], v, kTanh3[1]), v, kTanh3[0]);
+    return m.cap_out * (fabsf(x) > kTanhFewRange ? far : near);
+}
+
 // First visible key of the query at position p (may lie past p: nothing visible).
 __device__ __forceinline__ int first_key(const ScoreMods& m, int s, int p) {
     int lo = m.key_starts ? max(m.key_starts[s], 0) : 0;

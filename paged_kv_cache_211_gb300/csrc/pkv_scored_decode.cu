@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const float r = sa[x] + sb[x];
-                    z[x] = kCap ? md.cap_out * tanhf(r * md.cap_in) : r * md.scale_log2;
+                    z[x] = kCap ? cap_score(r, md) : r * md.scale_log2;
                     if (kBias)
                         z[x] = fmaf(slope[e][x & 1],
                                     (float)(t0 + gid + 8 * (x >> 1) - (n - 1)), z[x]);

@@ -58,14 +58,6 @@ static_assert(128 * kOtherRegs + kSoftWarps * 32 * kSoftmaxRegs <= kThreads * kL
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// tanh(x) / x as polynomials in x^2, fitted here by iterated weighted least
-// squares to the smallest largest relative error: four terms for |x| <= 0.5
-// (5.5e-7) and three for |x| <= 0.25 (4.0e-7).
-constexpr int kTanhTerms = 4, kTanhFew = 3;
-constexpr float kTanhRange = 0.5f, kTanhFewRange = 0.25f;
-constexpr float kTanh[kTanhTerms] = {0.999999456f, -0.333263179f, 0.131902966f, -0.0444022261f};
-constexpr float kTanhS[kTanhFew] = {0.999999604f, -0.333219082f, 0.128416134f};
-
 struct PrefillScored {
     const void* q;
     const void* k_cache;
@@ -211,11 +203,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float fast_rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&w)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(ptr),
                  "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
@@ -288,7 +275,7 @@ __device__ void plain_row(const PrefillScored& p, int s, int h, int head, int ro
             float dot = 0.f;
             const T* k = kc + slot * stride;
             for (int d = 0; d < D; ++d) dot = fmaf((float)q[d], (float)k[d], dot);
-            z = md.cap_out > 0.f ? md.cap_out * tanhf(dot * md.cap_in) : dot * md.scale_log2;
+            z = md.cap_out > 0.f ? cap_score(dot, md) : dot * md.scale_log2;
             z = fmaf(-slope, fabsf((float)(pos - t)), z);
         }
         float mx = z;
@@ -1218,9 +1205,9 @@ pkv_status paged_attention_prefill_scored(
         double f = prm.mods.scale_log2;
         bool ok = true;
         for (int i = 0; i < pkv::kTanhTerms; ++i, f *= c2) {
-            prm.tanh_z[i] = (float)(pkv::kTanh[i] * f);
+            prm.tanh_z[i] = (float)(pkv::kTanh4[i] * f);
             ok = ok && std::isnormal(prm.tanh_z[i]);
-            if (i < pkv::kTanhFew) prm.tanh_few[i] = (float)(pkv::kTanhS[i] * f);
+            if (i < pkv::kTanhFew) prm.tanh_few[i] = (float)(pkv::kTanh3[i] * f);
         }
         const float limit = pkv::kTanhRange / std::fabs(prm.mods.cap_in);
         if (ok && limit < 1e18f) {  // (its square is finite)
