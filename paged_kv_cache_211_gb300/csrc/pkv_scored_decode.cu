@@ -42,23 +42,22 @@ constexpr int kRowBlocks = 8;     // longest row (blocks) that a warp takes whol
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Per worker warp: where its first segment's row is joined.
-struct RowDesc {
-    int s, hg;          // s < 0: the worker's run starts at a row's first block
-    int first, last;    // workers that hold parts of the row
-    int first_slot;     // slot of the first worker's part (the others: 2 * worker)
-    int pad[3];
+// Where a row (sequence, head group) is joined.
+struct RowParts {
+    int first, last;   // workers that hold parts of it (equal: nothing to join)
+    int first_slot;    // slot of the first worker's part (the others: 2 * worker)
+    int pad;
 };
 
 struct Workspace {
-    size_t desc, ml, o, total;
+    size_t rows, ml, o, total;
 };
 
-Workspace ws_layout(int head_dim, int hps) {
+Workspace ws_layout(int num_rows, int head_dim, int hps) {
     const size_t workers = (size_t)kMaxCtas * kWarps;
     Workspace w;
-    w.desc = 0;
-    w.ml = align256(workers * sizeof(RowDesc));
+    w.rows = 0;
+    w.ml = align256((size_t)num_rows * sizeof(RowParts));
     w.o = w.ml + align256(2 * workers * hps * kMaxGroup * sizeof(float2));
     w.total = w.o + 2 * workers * hps * (head_dim / 16) * 32 * sizeof(float4);
     return w;
@@ -69,7 +68,7 @@ struct ScoredParams {
     void* out;
     const int32_t* block_tables;
     const int32_t* context_lens;
-    RowDesc* desc;
+    RowParts* rows;  // [num_seqs][head group]
     float2* ml;     // [slot][HPS][8]: m (base 2) and l of a query head
     float4* o;      // [slot][HPS][D / 16][lane]: accumulator fragments
     unsigned int* status;
@@ -277,32 +276,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (!rows_whole) {
-        // what the joining kernel needs to know of this worker's first row
-        if (lane == 0) {
-            RowDesc d = {};
-            d.s = -1;
-            if (u_begin < u_end) {
-                const int s = begin().s, nb = sm_off[s + 1] - sm_off[s];
-                const long long r = u_begin - (long long)HG * sm_off[s];
-                const int hg = (int)(r / nb);
-                if (r != (long long)hg * nb) {
-                    const long long row = (long long)HG * sm_off[s] + (long long)hg * nb;
-                    // the worker that holds unit u: the largest c with U c / workers <= u
-                    auto holder = [&](long long u) { return (int)(((u + 1) * workers - 1) / U); };
-                    d.s = s;
-                    d.hg = hg;
-                    d.first = holder(row);
-                    d.last = holder(row + nb - 1);
-                    d.first_slot = 2 * d.first + (U * d.first / workers < row ? 1 : 0);
-                }
-            }
-            p.desc[worker] = d;
-        }
         // sequences that see nothing: zeros
         for (int s = blockIdx.x; s < B; s += gridDim.x) {
             if (sm_lo[s] < sm_n[s]) continue;
             uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (size_t)s * Hq * D);
             for (int x = tid; x < Hq * D / 8; x += kThreads) o[x] = make_uint4(0u, 0u, 0u, 0u);
+            for (int x = tid; x < HG; x += kThreads) p.rows[(size_t)s * HG + x] = RowParts{};
         }
     }
 
@@ -367,6 +346,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool live = true;
     while (live && next(cc, sg)) {
         const int s = sg.s, n = sg.n, h0 = sg.hg * HPS;
+        if (!rows_whole && lane == 0 && sg.b == sg.lo / PKV_BLOCK_SIZE) {
+            // the row starts here: who shares it
+            RowParts r = {worker, worker, sg.slot, 0};
+            if (sg.slot >= 0) {
+                // the worker that holds the row's last unit u: the largest c with
+                // U c / workers <= u
+                const int nb = sm_off[s + 1] - sm_off[s];
+                const long long u = (long long)HG * sm_off[s] + (long long)(sg.hg + 1) * nb - 1;
+                r.last = (int)(((u + 1) * workers - 1) / U);
+            }
+            p.rows[(size_t)s * HG + sg.hg] = r;
+        }
         uint32_t qf[HPS][KS][2];
         float slope[HPS][2];
 #pragma unroll
@@ -537,81 +528,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the parts of one row (sequence, head group).  The CTA of worker w acts
-// if w is the second worker of the row its run starts in; warp (e, i) has
-// fragment i of head e from every part.
+// Joins the parts of the rows that several workers share, a row per CTA and
+// round; warp (e, i) has fragment i of head e from every part.
 constexpr int kFewParts = 6;
+constexpr int kJoinCtas = 4 * kMaxCtas;
 
 template <typename T, int D, int HPS>
 __global__ void __launch_bounds__(HPS * (D / 16) * 32)
-    scored_join_kernel(const RowDesc* __restrict__ desc, const float2* __restrict__ ml,
-                       const float4* __restrict__ o, void* out, int num_q_heads, int g) {
+    scored_join_kernel(const RowParts* __restrict__ rows, const float2* __restrict__ ml,
+                       const float4* __restrict__ o, void* out, int num_rows, int num_q_heads,
+                       int g) {
     constexpr int KS = D / 16;
     // the next kernel's CTAs may be scheduled beside these; it waits for this
     // grid before it touches anything (griddepcontrol.wait)
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const RowDesc d = desc[blockIdx.x];
-    if (d.s < 0 || d.first + 1 != (int)blockIdx.x) return;
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     const int e = (threadIdx.x >> 5) / KS, i = (threadIdx.x >> 5) % KS;
     const bool has = 2 * tig < g;
-    auto slot_of = [&](int c) { return c == d.first ? d.first_slot : 2 * c; };
-    auto ml_of = [&](int c) {  // m, l of heads 2 tig and 2 tig + 1
-        return *reinterpret_cast<const float4*>(ml + ((size_t)slot_of(c) * HPS + e) * kMaxGroup +
-                                                2 * tig);
-    };
-    auto o_of = [&](int c) { return o[(((size_t)slot_of(c) * HPS + e) * KS + i) * 32 + lane]; };
-    float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4& v, const float4& x) {
-        const float w0 = fast_exp2(v.x - M0), w1 = fast_exp2(v.z - M1);
-        L0 += w0 * v.y;
-        L1 += w1 * v.w;
-        acc.x += w0 * x.x;
-        acc.y += w1 * x.y;
-        acc.z += w0 * x.z;
-        acc.w += w1 * x.w;
-    };
-    if (d.last - d.first < kFewParts) {  // (uniform) every load at once
-        float4 v[kFewParts], x[kFewParts];
+    const int HG = num_q_heads / g / HPS;
+    for (int row = blockIdx.x; row < num_rows; row += gridDim.x) {
+        const RowParts d = rows[row];
+        if (d.first == d.last) continue;
+        auto slot_of = [&](int c) { return c == d.first ? d.first_slot : 2 * c; };
+        auto ml_of = [&](int c) {  // m, l of heads 2 tig and 2 tig + 1
+            return *reinterpret_cast<const float4*>(ml + ((size_t)slot_of(c) * HPS + e) * kMaxGroup +
+                                                    2 * tig);
+        };
+        auto o_of = [&](int c) { return o[(((size_t)slot_of(c) * HPS + e) * KS + i) * 32 + lane]; };
+        float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4& v, const float4& x) {
+            const float w0 = fast_exp2(v.x - M0), w1 = fast_exp2(v.z - M1);
+            L0 += w0 * v.y;
+            L1 += w1 * v.w;
+            acc.x += w0 * x.x;
+            acc.y += w1 * x.y;
+            acc.z += w0 * x.z;
+            acc.w += w1 * x.w;
+        };
+        if (d.last - d.first < kFewParts) {  // (uniform) every load at once
+            float4 v[kFewParts], x[kFewParts];
 #pragma unroll
-        for (int k = 0; k < kFewParts; ++k) {
-            const bool here = has && d.first + k <= d.last;
-            v[k] = here ? ml_of(d.first + k) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-            x[k] = here ? o_of(d.first + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+            for (int k = 0; k < kFewParts; ++k) {
+                const bool here = has && d.first + k <= d.last;
+                v[k] = here ? ml_of(d.first + k) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                x[k] = here ? o_of(d.first + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
 #pragma unroll
-        for (int k = 0; k < kFewParts; ++k) {
-            M0 = fmaxf(M0, v[k].x);
-            M1 = fmaxf(M1, v[k].z);
-        }
-        if (M0 == -INFINITY) M0 = 0.f;
-        if (M1 == -INFINITY) M1 = 0.f;
+            for (int k = 0; k < kFewParts; ++k) {
+                M0 = fmaxf(M0, v[k].x);
+                M1 = fmaxf(M1, v[k].z);
+            }
+            if (M0 == -INFINITY) M0 = 0.f;
+            if (M1 == -INFINITY) M1 = 0.f;
 #pragma unroll
-        for (int k = 0; k < kFewParts; ++k) add(v[k], x[k]);
-    } else {
-        for (int c = d.first + gid; has && c <= d.last; c += 8) {
-            const float4 v = ml_of(c);
-            M0 = fmaxf(M0, v.x);
-            M1 = fmaxf(M1, v.z);
-        }
+            for (int k = 0; k < kFewParts; ++k) add(v[k], x[k]);
+        } else {
+            for (int c = d.first + gid; has && c <= d.last; c += 8) {
+                const float4 v = ml_of(c);
+                M0 = fmaxf(M0, v.x);
+                M1 = fmaxf(M1, v.z);
+            }
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, off));
-            M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, off));
-        }
-        if (M0 == -INFINITY) M0 = 0.f;
-        if (M1 == -INFINITY) M1 = 0.f;
-        if (has) {
+            for (int off = 4; off < 32; off <<= 1) {
+                M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, off));
+                M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, off));
+            }
+            if (M0 == -INFINITY) M0 = 0.f;
+            if (M1 == -INFINITY) M1 = 0.f;
+            if (has) {
 #pragma unroll 8
-            for (int c = d.first; c <= d.last; ++c) add(ml_of(c), o_of(c));
+                for (int c = d.first; c <= d.last; ++c) add(ml_of(c), o_of(c));
+            }
         }
+        const float inv0 = L0 != 0.f ? 1.f / L0 : 0.f, inv1 = L1 != 0.f ? 1.f / L1 : 0.f;
+        const int s = row / HG, hg = row - s * HG;
+        T* head0 = static_cast<T*>(out) + ((size_t)s * num_q_heads + (size_t)(hg * HPS + e) * g) * D;
+        store_fragment(head0, D, 16 * i, g, acc.x, acc.y, acc.z, acc.w, inv0, inv1);
     }
-    const float inv0 = L0 != 0.f ? 1.f / L0 : 0.f, inv1 = L1 != 0.f ? 1.f / L1 : 0.f;
-    T* head0 = static_cast<T*>(out) +
-               ((size_t)d.s * num_q_heads + (size_t)(d.hg * HPS + e) * g) * D;
-    store_fragment(head0, D, 16 * i, g, acc.x, acc.y, acc.z, acc.w, inv0, inv1);
 }
 
 int heads_per_step(int head_dim, int num_kv_heads) {
@@ -637,12 +632,13 @@ pkv_status launch_scored(const ScoredParams& prm, const CUtensorMap& tmk, const 
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, prm, tmk, tmv) != cudaSuccess) return PKV_ERR_CUDA;
     if (prm.rows_whole) return PKV_OK;
-    cfg.gridDim = dim3((unsigned)(ctas * kWarps));
+    const int rows = prm.num_seqs * (prm.num_kv_heads / HPS);
+    cfg.gridDim = dim3((unsigned)std::min(rows, kJoinCtas));
     cfg.blockDim = dim3(HPS * (D / 16) * 32);
     cfg.dynamicSmemBytes = 0;
     return cuda_status(cudaLaunchKernelEx(&cfg, scored_join_kernel<T, D, HPS>,
-                                          (const RowDesc*)prm.desc, (const float2*)prm.ml,
-                                          (const float4*)prm.o, prm.out, prm.num_q_heads,
+                                          (const RowParts*)prm.rows, (const float2*)prm.ml,
+                                          (const float4*)prm.o, prm.out, rows, prm.num_q_heads,
                                           prm.group));
 }
 
@@ -656,8 +652,8 @@ pkv_status launch_scored_mods(ScoredParams prm, const void* k_cache, const void*
     const int sms = sm_count();
     if (sms <= 0) return PKV_ERR_CUDA;
     const int ctas = std::min(sms, kMaxCtas);
-    const Workspace ws = ws_layout(D, HPS);
-    prm.desc = reinterpret_cast<RowDesc*>(workspace + ws.desc);
+    const Workspace ws = ws_layout(prm.num_seqs * (prm.num_kv_heads / HPS), D, HPS);
+    prm.rows = reinterpret_cast<RowParts*>(workspace + ws.rows);
     prm.ml = reinterpret_cast<float2*>(workspace + ws.ml);
     prm.o = reinterpret_cast<float4*>(workspace + ws.o);
     // three stages a warp where the lengths leave room for them (up to ~2900
@@ -697,7 +693,10 @@ size_t paged_attention_decode_scored_workspace_bytes(int num_seqs, int num_q_hea
     if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_context_len < 0 ||
         num_q_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128))
         return 0;
-    return pkv::ws_layout(head_dim, pkv::heads_per_step(head_dim, num_kv_heads)).total;
+    const int hps = pkv::heads_per_step(head_dim, num_kv_heads);
+    const long long rows = (long long)num_seqs * (num_kv_heads / hps);
+    if (rows > 0x7fffffffll) return 0;
+    return pkv::ws_layout((int)rows, head_dim, hps).total;
 }
 
 pkv_status paged_attention_decode_scored(
@@ -728,6 +727,7 @@ pkv_status paged_attention_decode_scored(
         return PKV_ERR_INVALID_ARG;
     const size_t need = paged_attention_decode_scored_workspace_bytes(
         num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len);
+    if (need == 0) return PKV_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return PKV_ERR_WORKSPACE;
     prm.status = pkv::status_word();
