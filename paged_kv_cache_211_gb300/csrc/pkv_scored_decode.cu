@@ -96,6 +96,19 @@ __device__ __forceinline__ Span span_of(const ScoredParams& p, int s, bool repor
     return r;
 }
 
+// a * b / c and a / b, in 32 bits where they fit (a 64-bit division takes some
+// hundred instructions; the walks do a dozen before the first copy).
+__device__ __forceinline__ long long mul_div(long long a, int b, int c) {
+    const unsigned long long x = (unsigned long long)a * (unsigned)b;
+    return (x >> 32) == 0 ? (long long)((unsigned)x / (unsigned)c)
+                          : (long long)(x / (unsigned)c);
+}
+__device__ __forceinline__ int div_int(long long a, long long b) {
+    return (((unsigned long long)a | (unsigned long long)b) >> 32) == 0
+               ? (int)((unsigned)a / (unsigned)b)
+               : (int)(a / b);
+}
+
 // K and V pools as (element, row, 64-element half, head): one box is a stage's
 // tile, [head][half][16 rows][128 bytes] in shared memory.
 __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, uint64_t* bar, int row,
@@ -166,7 +179,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (lane == 0)
         for (int k = 0; k < NS; ++k) mbar_init(&full[warp * NS + k], 1);
-    if (tid == 0) abort_word = 0;
+    if (tid == 0) {
+        abort_word = 0;
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
+    }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     // a programmatic dependent: nothing of the caller's is touched before the
     // kernel in front of this one is complete
@@ -226,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s;
     };
     const bool idle = !rows_whole && worker >= workers;
-    const long long u_end = rows_whole ? (long long)B * HG : idle ? 0 : U * (worker + 1) / workers;
-    const long long u_begin = rows_whole ? worker : idle ? 0 : U * worker / workers;
+    const long long u_end = rows_whole ? (long long)B * HG : idle ? 0 : mul_div(U, worker + 1, workers);
+    const long long u_begin = rows_whole ? worker : idle ? 0 : mul_div(U, worker, workers);
     auto begin = [&]() {
         Cursor c = {u_begin, 0};
         if (!rows_whole && u_begin < u_end) {  // the sequence that holds unit u_begin
@@ -256,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int s = c.s, nb = sm_off[s + 1] - sm_off[s];
         const long long r = c.u - (long long)HG * sm_off[s];
-        const int hg = (int)(r / nb), k = (int)(r - (long long)hg * nb);
+        const int hg = div_int(r, nb), k = (int)(r - (long long)hg * nb);
         const long long left = u_end - c.u;
         const int len = nb - k < left ? nb - k : (int)left;
         g_.s = s;
@@ -354,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // U c / workers <= u
                 const int nb = sm_off[s + 1] - sm_off[s];
                 const long long u = (long long)HG * sm_off[s] + (long long)(sg.hg + 1) * nb - 1;
-                r.last = (int)(((u + 1) * workers - 1) / U);
+                r.last = div_int((u + 1) * workers - 1, U);
             }
             p.rows[(size_t)s * HG + sg.hg] = r;
         }
