@@ -129,18 +129,14 @@ __device__ __forceinline__ bool token_place(const RopeParams& p, int t, bool rep
 // One CTA per token.  Thread (x, y): x is a unit of a head row -- V pairs of
 // the rotated part (half layout: V elements at j and V at j + R/2; interleaved:
 // V elements, V/2 pairs) or V copied elements -- and the same for every head,
-// so a thread keeps its V cosines and sines in registers while it walks the
+// so a thread uses the same V cosines and sines while it walks the
 // token's Hq + 2 Hkv head rows (q, k, v; v's units are copied) in steps of
 // blockDim.y.  The first rows' loads are issued before the angles are formed.
 template <typename T, bool kInterleaved, int V>
-__global__ void __launch_bounds__(kRopeMaxDim) rope_write_kernel(const RopeParams p) {
-    __shared__ float sm_cos[kRopeMaxDim / 2], sm_sin[kRopeMaxDim / 2];
+__global__ void __launch_bounds__(kRopeMaxDim, 2) rope_write_kernel(const RopeParams p) {
+    __shared__ __align__(16) float sm_cos[kRopeMaxDim / 2], sm_sin[kRopeMaxDim / 2];
     const int t = blockIdx.x;
     const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-    int pos = 0;
-    int64_t slot;
-    if (!token_place(p, t, tid == 0, pos, slot)) return;  // uniform over the CTA
-
     const int D = p.head_dim, R = p.rotary_dim, half = R / 2;
     const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, rows = Hq + 2 * Hkv;
     // this thread's unit: first element(s), and its first cosine
@@ -157,6 +153,7 @@ __global__ void __launch_bounds__(kRopeMaxDim) rope_write_kernel(const RopeParam
             return static_cast<const T*>(p.k_new) + t * p.k_stride + (int64_t)(r - Hq) * D;
         return static_cast<const T*>(p.v_new) + t * p.v_stride + (int64_t)(r - Hq - Hkv) * D;
     };
+    int64_t slot;
     auto target = [&](int r) -> T* {
         if (r < Hq) return static_cast<T*>(p.q_out) + ((int64_t)t * Hq + r) * D;
         if (r < Hq + Hkv) return static_cast<T*>(p.k_cache) + (slot * Hkv + r - Hq) * D;
@@ -174,20 +171,14 @@ __global__ void __launch_bounds__(kRopeMaxDim) rope_write_kernel(const RopeParam
             if (pair) b[i].w = *reinterpret_cast<const decltype(a[i].w)*>(src + e1);
         }
     };
-    load(threadIdx.y);
+    load(threadIdx.y);  // (a padding token's rows are there too)
+    int pos = 0;
+    if (!token_place(p, t, tid == 0, pos, slot)) return;  // uniform over the CTA
     for (int j = tid; j < half; j += blockDim.x * blockDim.y)
         rotation(pos, p.inv_freq[j], p.rope_scale, sm_cos[j], sm_sin[j]);
     __syncthreads();
-    constexpr int NC = kInterleaved ? (V + 1) / 2 : V;  // pairs of a unit
-    float c[NC], s[NC];
-    if (rotated) {
-        const int j0 = kInterleaved ? e0 / 2 : e0;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            c[i] = sm_cos[j0 + i];
-            s[i] = sm_sin[j0 + i];
-        }
-    }
+    const float* c = sm_cos + (kInterleaved ? e0 / 2 : e0);  // (rotated units only)
+    const float* s = sm_sin + (kInterleaved ? e0 / 2 : e0);
     for (int r0 = threadIdx.y; r0 < rows; r0 += kRopeBatch * blockDim.y) {
         if (r0 != (int)threadIdx.y) load(r0);
 #pragma unroll
