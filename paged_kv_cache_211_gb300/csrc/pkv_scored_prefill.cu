@@ -72,6 +72,7 @@ struct PrefillScored {
     int max_q_len, num_q_rows;
     int pairs_per_seq;     // ceil(max_q_len * group / kPair)
     int splits;            // key runs per item; > 1: partials go to the workspace
+    int sorted;            // deal the items that hold rows, by their number of key tiles
     // the polynomials' terms, z = raw sum tanh_z[i] raw^2i, and the largest |raw
     // score| that each serves (negative: none)
     float tanh_z[kTanhTerms], tanh_few[kTanhFew];
@@ -110,18 +111,14 @@ __device__ __forceinline__ int row_lo(const PrefillScored& p, const Item& it, in
 }
 __device__ __forceinline__ int row_hi(const Item& it, int pos) { return max(pos + 1, it.prefix); }
 
-// Item i, heaviest first (pairs from the end of each chunk, where the causal
-// range is longest); false if it holds no rows or its lengths are invalid
-// (flagged once per sequence).
-__device__ __forceinline__ bool item_at(const PrefillScored& p, int i, bool flag, Item& it) {
-    const int per_pair = p.num_seqs * p.num_kv_heads * p.splits;
-    const int pair = p.pairs_per_seq - 1 - i / per_pair;
-    int rem = i % per_pair;
-    it.split = rem % p.splits;
-    rem /= p.splits;
-    it.s = rem / p.num_kv_heads;
-    it.h = rem - it.s * p.num_kv_heads;
-    it.base = (it.s * p.num_kv_heads + it.h) * p.pairs_per_seq + pair;
+// The item of these coordinates; false (nkv = -1) if it holds no rows or its
+// lengths are invalid (flagged once per sequence).
+__device__ __forceinline__ bool item_at(const PrefillScored& p, int s, int pair, int h, int split,
+                                        bool flag, Item& it) {
+    it.split = split;
+    it.s = s;
+    it.h = h;
+    it.base = (s * p.num_kv_heads + h) * p.pairs_per_seq + pair;
     it.q0 = p.cu_q_lens[it.s];
     it.qlen = p.cu_q_lens[it.s + 1] - it.q0;
     it.n = p.context_lens[it.s];
@@ -155,6 +152,15 @@ __device__ __forceinline__ bool item_at(const PrefillScored& p, int i, bool flag
     return true;
 }
 
+// Item i of the plain order: pairs from the end of each chunk first, where the
+// causal range is longest.
+__device__ __forceinline__ bool plain_item(const PrefillScored& p, int i, bool flag, Item& it) {
+    const int per_pair = p.num_seqs * p.num_kv_heads * p.splits;
+    const int pair = p.pairs_per_seq - 1 - i / per_pair;
+    const int rem = i % per_pair, sh = rem / p.splits, s = sh / p.num_kv_heads;
+    return item_at(p, s, pair, sh - s * p.num_kv_heads, rem - sh * p.splits, flag, it);
+}
+
 // The item this CTA takes in round r: rounds alternate direction over the
 // CTAs, so that heaviest-first items even out.
 __device__ __forceinline__ int round_item(int r) {
@@ -170,7 +176,67 @@ __device__ __forceinline__ bool round_at(const PrefillScored& p, const Item* tab
         return it.nkv >= 0;
     }
     const int i = round_item(r);
-    return i < num_items && item_at(p, i, flag, it);
+    return i < num_items && plain_item(p, i, flag, it);
+}
+
+// The (sequence, pair) entries that hold rows, those with the most key tiles
+// first (a stable counting sort, the same in every CTA), in order[]; returns how
+// many.  Ragged chunks leave most entries without rows and the others of very
+// different cost: dealt in the plain order, the busiest CTA of 24 chunks of 1 to
+// 700 tokens held three items of 184, where two would do.  By the whole CTA,
+// with scratch of kSortMax + 2 * kSortKeys words.
+constexpr int kSortMax = 1024;   // entries
+constexpr int kSortKeys = 256;   // key tiles told apart
+
+__device__ int sort_entries(const PrefillScored& p, int* scratch, uint16_t* order) {
+    const int E = p.num_seqs * p.pairs_per_seq;
+    int* key = scratch;                  // [E] kSortKeys - 1 - tiles; kSortKeys: no rows
+    int* offset = scratch + kSortMax;    // [kSortKeys + 1]
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int k = tid; k <= kSortKeys; k += kThreads) offset[k] = 0;
+    __syncthreads();
+    for (int e = tid; e < E; e += kThreads) {
+        const int s = e / p.pairs_per_seq;
+        Item it;
+        // (whole items: a split's share of the tiles orders them alike)
+        const bool any = item_at(p, s, e - s * p.pairs_per_seq, 0, 0, blockIdx.x == 0, it);
+        key[e] = any ? kSortKeys - 1 - min(it.nkv, kSortKeys - 1) : kSortKeys;
+        if (any) atomicAdd(&offset[key[e]], 1);
+    }
+    __syncthreads();
+    if (tid < 32) {
+        // counts to offsets, eight keys a lane
+        constexpr int PER = kSortKeys / 32;
+        int mine = 0;
+        for (int k = 0; k < PER; ++k) mine += offset[lane * PER + k];
+        int run = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += u;
+        }
+        const int total = __shfl_sync(0xffffffffu, run, 31);
+        run -= mine;
+        for (int k = 0; k < PER; ++k) {
+            const int c = offset[lane * PER + k];
+            offset[lane * PER + k] = run;
+            run += c;
+        }
+        if (lane == 0) offset[kSortKeys] = total;
+        __syncwarp();
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane, k = e < E ? key[e] : kSortKeys;
+            const unsigned same = __match_any_sync(0xffffffffu, k);
+            const int at = k < kSortKeys ? offset[k] + __popc(same & ((1u << lane) - 1u)) : 0;
+            __syncwarp();
+            if (k < kSortKeys) {
+                order[at] = (uint16_t)e;
+                if ((same >> lane) == 1u) offset[k] = at + 1;  // the key's last lane
+            }
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    return offset[kSortKeys];
 }
 
 // Two-wide fp32 arithmetic on packed register pairs, the three-input maximum
@@ -444,14 +510,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 2) tc_alloc(tmem_slot, kCols);
+    // the items (the tiles' memory is still free: the sort's scratch)
+    uint16_t* order = reinterpret_cast<uint16_t*>(sk);
+    const int per_entry = p.num_kv_heads * p.splits;
+    if (p.sorted) num_items = per_entry * sort_entries(p, reinterpret_cast<int*>(sq), order);
     const int rounds = (num_items + (int)gridDim.x - 1) / (int)gridDim.x;
-    if (tid < min(rounds, kItemCache)) {
+    for (int r = tid; r < min(rounds, kItemCache); r += kThreads) {
         Item it;
         it.nkv = -1;
-        const int i = round_item(tid);
-        if (i < num_items) item_at(p, i, true, it);
-        table[tid] = it;
+        const int i = round_item(r);
+        if (i < num_items) {
+            if (p.sorted) {
+                const int e = order[i / per_entry], s = e / p.pairs_per_seq;
+                const int rem = i % per_entry, h = rem / p.splits;
+                item_at(p, s, e - s * p.pairs_per_seq, h, rem - h * p.splits, false, it);
+            } else {
+                plain_item(p, i, true, it);
+            }
+        }
+        table[r] = it;
     }
+    // (copies will overwrite the scratch)
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1198,6 +1278,11 @@ pkv_status paged_attention_prefill_scored(
     prm.num_q_rows = num_q_rows;
     prm.pairs_per_seq = pl.pairs;
     prm.splits = pl.splits;
+    // worth its 1 to 2 us where a CTA may get several items, possible where the
+    // entries fit the scratch and the CTA's table all of its items
+    const long long entries = (long long)num_seqs * pl.pairs;
+    prm.sorted = pl.items * pl.splits > ctas && entries <= pkv::kSortMax &&
+                 pl.items * pl.splits <= (long long)pkv::kItemCache * ctas;
     // z = cap' x (tanh(x) / x) with x = raw cap_in: the terms in raw^2, times cap' cap_in
     prm.tanh_limit = prm.tanh_few_limit = -1.f;
     if (softcap > 0.f && scale != 0.f) {
