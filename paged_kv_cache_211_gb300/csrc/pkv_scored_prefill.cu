@@ -510,6 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 2) tc_alloc(tmem_slot, kCols);
+    // the joining kernel may be scheduled as this grid's CTAs leave (the kernel
+    // in front of this one, an ordinary launch's, is complete)
+    if (p.splits > 1) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     // the items (the tiles' memory is still free: the sort's scratch)
     uint16_t* order = reinterpret_cast<uint16_t*>(sk);
     const int per_entry = p.num_kv_heads * p.splits;
@@ -1079,47 +1082,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the splits of one item's rows, a warp per row:
 //   M = max m,  out = sum o 2^(m - M) / sum l 2^(m - M).
+// Lane k has split k's m and l (at most 32 splits); the o of eight splits are in
+// flight at a time.  A programmatic dependent of the kernel above.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 32;  // rows of an item per CTA
+constexpr int kJoinRows = 8;   // rows of an item per CTA: a warp each
+constexpr int kMaxSplits = 32;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) scored_prefill_join_kernel(const PrefillScored p) {
     constexpr int PER = D / 32;
-    const int base = blockIdx.x / (kPair / kJoinRows);
-    const int pair = base % p.pairs_per_seq;
-    const int h = base / p.pairs_per_seq % p.num_kv_heads;
-    const int s = base / p.pairs_per_seq / p.num_kv_heads;
-    const int q0 = p.cu_q_lens[s], qlen = p.cu_q_lens[s + 1] - q0, n = p.context_lens[s];
-    if (!lengths_ok(p, q0, qlen, n)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = p.group, S = p.splits;
-    const int r0 = blockIdx.x % (kPair / kJoinRows) * kJoinRows;
-    for (int r = r0 + warp; r < r0 + kJoinRows; r += kJoinWarps) {
-        const int R = pair * kPair + r;
-        if (R >= qlen * g) return;
-        const int t = R / g, head = h * g + R - t * g;
-        const size_t row = (size_t)base * S * kPair + r;
-        float M = -INFINITY;
-        for (int k = 0; k < S; ++k) M = fmaxf(M, p.ws_m[row + (size_t)k * kPair]);
-        if (M == -INFINITY) M = 0.f;
-        float L = 0.f, acc[PER];
+    const int base = blockIdx.x / (kPair / kJoinRows);
+    const int r = blockIdx.x % (kPair / kJoinRows) * kJoinRows + warp;
+    const int sh = base / p.pairs_per_seq, pair = base - sh * p.pairs_per_seq;
+    const int s = sh / p.num_kv_heads, h = sh - s * p.num_kv_heads;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int q0 = p.cu_q_lens[s], qlen = p.cu_q_lens[s + 1] - q0, n = p.context_lens[s];
+    const int R = pair * kPair + r;
+    if (!lengths_ok(p, q0, qlen, n) || R >= qlen * g) return;
+    const size_t row = (size_t)base * S * kPair + r;
+    const float m = lane < S ? p.ws_m[row + (size_t)lane * kPair] : -INFINITY;
+    const float l = lane < S ? p.ws_l[row + (size_t)lane * kPair] : 0.f;
+    float M = m;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-        for (int k = 0; k < S; ++k) {
-            const size_t kr = row + (size_t)k * kPair;
-            const float lk = p.ws_l[kr];
-            if (lk == 0.f) continue;  // a split without visible keys wrote no o
-            const float w = fast_exp2(p.ws_m[kr] - M);
-            L += w * lk;
-            const float* o = p.ws_o + kr * D + lane * PER;
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (M == -INFINITY) M = 0.f;
+    // (a split without visible keys, l = 0, wrote no o)
+    const float w = l != 0.f ? fast_exp2(m - M) : 0.f;
+    float L = w * l, acc[PER];
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, o[e], acc[e]);
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    const unsigned some = __ballot_sync(0xffffffffu, l != 0.f);
+    const float* o0 = p.ws_o + row * D + lane * PER;
+#pragma unroll 1
+    for (int k0 = 0; k0 < S; k0 += 8) {
+        float x[8][PER];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                x[k][e] = (some >> (k0 + k)) & 1u ? o0[(size_t)(k0 + k) * kPair * D + e] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(wk, x[k][e], acc[e]);
         }
-        const float inv = L != 0.f ? 1.f / L : 0.f;
-        T* dst = static_cast<T*>(p.out) + ((size_t)(q0 + t) * p.num_q_heads + head) * D + lane * PER;
-#pragma unroll
-        for (int e = 0; e < PER; e += 2)
-            *reinterpret_cast<uint32_t*>(dst + e) = Elem<T>::pack(acc[e] * inv, acc[e + 1] * inv);
     }
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    const int t = R / g, head = h * g + R - t * g;
+    T* dst = static_cast<T*>(p.out) + ((size_t)(q0 + t) * p.num_q_heads + head) * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = Elem<T>::pack(acc[e] * inv, acc[e + 1] * inv);
 }
 
 // Items before splitting, and into how many key runs each is cut: enough for
@@ -1135,7 +1152,8 @@ Plan make_plan(int num_seqs, int max_q_len, int num_kv_heads, int group, int cta
     pl.pairs = (int)(((long long)max_q_len * group + kPair - 1) / kPair);
     pl.items = (long long)num_seqs * num_kv_heads * pl.pairs;
     const long long by_ctas = pl.items > 0 ? ctas / pl.items : 1;
-    pl.splits = (int)std::max<long long>(1, std::min(by_ctas, max_tiles / 2));
+    pl.splits =
+        (int)std::max<long long>(1, std::min({by_ctas, max_tiles / 2, (long long)kMaxSplits}));
     return pl;
 }
 
@@ -1177,9 +1195,16 @@ pkv_status launch(const PrefillScored& prm, const CUtensorMap& tmk, const CUtens
     kern<<<std::min(items, ctas), kThreads, smem, stream>>>(prm, tmk, tmv, tmq, q_tma, items);
     if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
     if (prm.splits == 1) return PKV_OK;
-    scored_prefill_join_kernel<T, D>
-        <<<items / prm.splits * (kPair / kJoinRows), kJoinWarps * 32, 0, stream>>>(prm);
-    return cuda_status(cudaGetLastError());
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items / prm.splits * (kPair / kJoinRows)));
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, scored_prefill_join_kernel<T, D>, prm));
 }
 
 template <typename T, int D>
