@@ -17,6 +17,7 @@
 // For |p| < 2^24 the turns are within 2^-23 of the exact ones; sincospif does
 // the rest.  (64-bit products cost more: 64 lanes' worth of them per token
 // share an FP64 pipe of two lanes an SM.)
+#include <algorithm>
 #include <cmath>
 
 #include "pkv_internal.cuh"
@@ -26,7 +27,7 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeMaxDim = 512;   // head_dim
-constexpr int kRopeBatch = 4;      // head rows a thread has in flight
+constexpr int kRopeBatch = 2;      // head rows a thread has in flight
 
 struct RopeParams {
     const void* q;
@@ -50,27 +51,17 @@ struct RopeParams {
     unsigned int* status;
 };
 
-template <int BYTES>
-struct Word;
-template <>
-struct Word<16> { using type = uint4; };
-template <>
-struct Word<8> { using type = uint2; };
-template <>
-struct Word<4> { using type = uint32_t; };
-template <>
-struct Word<2> { using type = uint16_t; };
-
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ void from_f32(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f32(__half& d, float x) { d = __float2half_rn(x); }
 
-// V consecutive elements of a row, moved as one word.
-template <typename T, int V>
+constexpr int kVec = 8;  // elements of a 16-byte word
+
+template <typename T>
 union Vec {
-    typename Word<V * (int)sizeof(T)>::type w;
-    T e[V];
+    uint4 w;
+    T e[kVec];
     __device__ __forceinline__ Vec() {}
 };
 
@@ -126,53 +117,68 @@ __device__ __forceinline__ bool token_place(const RopeParams& p, int t, bool rep
     return slot >= 0;
 }
 
-// One CTA per token.  Thread (x, y): x is a unit of a head row -- V pairs of
-// the rotated part (half layout: V elements at j and V at j + R/2; interleaved:
-// V elements, V/2 pairs) or V copied elements -- and the same for every head,
-// so a thread uses the same V cosines and sines while it walks the
-// token's Hq + 2 Hkv head rows (q, k, v; v's units are copied) in steps of
-// blockDim.y.  The first rows' loads are issued before the angles are formed.
-template <typename T, bool kInterleaved, int V>
-__global__ void __launch_bounds__(kRopeMaxDim, 2) rope_write_kernel(const RopeParams p) {
+// Row r of a token's Hq + 2 Hkv head rows: where it comes from and goes to.
+template <typename T>
+struct TokenRows {
+    const RopeParams& p;
+    int t;
+    __device__ __forceinline__ const T* source(int r) const {
+        if (r < p.num_q_heads)
+            return static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)r * p.head_dim;
+        r -= p.num_q_heads;
+        if (r < p.num_kv_heads)
+            return static_cast<const T*>(p.k_new) + t * p.k_stride + (int64_t)r * p.head_dim;
+        return static_cast<const T*>(p.v_new) + t * p.v_stride +
+               (int64_t)(r - p.num_kv_heads) * p.head_dim;
+    }
+    __device__ __forceinline__ T* target(int r, int64_t slot) const {
+        if (r < p.num_q_heads)
+            return static_cast<T*>(p.q_out) + ((int64_t)t * p.num_q_heads + r) * p.head_dim;
+        r -= p.num_q_heads;
+        if (r < p.num_kv_heads)
+            return static_cast<T*>(p.k_cache) + (slot * p.num_kv_heads + r) * p.head_dim;
+        return static_cast<T*>(p.v_cache) +
+               (slot * p.num_kv_heads + r - p.num_kv_heads) * p.head_dim;
+    }
+};
+
+// One CTA per token.  Thread (x, y): x is a unit of a head row -- interleaved:
+// one 16-byte word; half layout: the word at j and its partner at j + R / 2, or a
+// copied word -- and the same for every head, so a thread uses the same cosines
+// and sines while it walks the token's head rows (q, k, v; v's units are copied)
+// in steps of blockDim.y.  The first rows' loads are issued before the token's
+// slot is known and before the angles are formed.
+// HBM bound: 2 (Hq + 2 Hkv) D elements read and written per token.  16384
+// tokens of 32q/8kv heads of 128: 60.7 us, 6.65 TB/s.
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeMaxDim, 3) rope_write_kernel(const RopeParams p) {
     __shared__ __align__(16) float sm_cos[kRopeMaxDim / 2], sm_sin[kRopeMaxDim / 2];
     const int t = blockIdx.x;
     const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-    const int D = p.head_dim, R = p.rotary_dim, half = R / 2;
-    const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, rows = Hq + 2 * Hkv;
-    // this thread's unit: first element(s), and its first cosine
+    const TokenRows<T> rows_of = {p, t};
+    const int R = p.rotary_dim, half = R / 2;
+    const int rotated_rows = p.num_q_heads + p.num_kv_heads;
+    const int rows = rotated_rows + p.num_kv_heads;
+    // this thread's unit: its first element(s)
     const int x = threadIdx.x;
-    const int rot_units = (kInterleaved ? R : half) / V;
-    const bool rotated = x < rot_units;
-    const int e0 = rotated ? x * V : R + (x - rot_units) * V;
-    const int e1 = e0 + half;                        // the half layout's partner elements
-    const bool pair = !kInterleaved && rotated;
+    const bool pair = !kInterleaved && x < half / kVec;
+    const int e0 = kInterleaved || pair ? x * kVec : R + (x - half / kVec) * kVec;
+    const int e1 = e0 + half;  // the half layout's partner elements
 
-    auto source = [&](int r) -> const T* {
-        if (r < Hq) return static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)r * D;
-        if (r < Hq + Hkv)
-            return static_cast<const T*>(p.k_new) + t * p.k_stride + (int64_t)(r - Hq) * D;
-        return static_cast<const T*>(p.v_new) + t * p.v_stride + (int64_t)(r - Hq - Hkv) * D;
-    };
-    int64_t slot;
-    auto target = [&](int r) -> T* {
-        if (r < Hq) return static_cast<T*>(p.q_out) + ((int64_t)t * Hq + r) * D;
-        if (r < Hq + Hkv) return static_cast<T*>(p.k_cache) + (slot * Hkv + r - Hq) * D;
-        return static_cast<T*>(p.v_cache) + (slot * Hkv + r - Hq - Hkv) * D;
-    };
-
-    Vec<T, V> a[kRopeBatch], b[kRopeBatch];
+    Vec<T> a[kRopeBatch], b[kRopeBatch];
     auto load = [&](int r0) {
 #pragma unroll
         for (int i = 0; i < kRopeBatch; ++i) {
             const int r = r0 + i * (int)blockDim.y;
             if (r >= rows) continue;
-            const T* src = source(r);
-            a[i].w = *reinterpret_cast<const decltype(a[i].w)*>(src + e0);
-            if (pair) b[i].w = *reinterpret_cast<const decltype(a[i].w)*>(src + e1);
+            const T* src = rows_of.source(r);
+            a[i].w = *reinterpret_cast<const uint4*>(src + e0);
+            if (pair) b[i].w = *reinterpret_cast<const uint4*>(src + e1);
         }
     };
     load(threadIdx.y);  // (a padding token's rows are there too)
     int pos = 0;
+    int64_t slot;
     if (!token_place(p, t, tid == 0, pos, slot)) return;  // uniform over the CTA
     for (int j = tid; j < half; j += blockDim.x * blockDim.y)
         rotation(pos, p.inv_freq[j], p.rope_scale, sm_cos[j], sm_sin[j]);
@@ -185,56 +191,130 @@ __global__ void __launch_bounds__(kRopeMaxDim, 2) rope_write_kernel(const RopePa
         for (int i = 0; i < kRopeBatch; ++i) {
             const int r = r0 + i * (int)blockDim.y;
             if (r >= rows) continue;
-            if (rotated && r < Hq + Hkv) {
+            if (r < rotated_rows) {
                 if constexpr (kInterleaved) {
 #pragma unroll
-                    for (int u = 0; u < V / 2; ++u) {
+                    for (int u = 0; u < kVec / 2; ++u) {
+                        if (e0 + 2 * u >= R) continue;  // (R may end inside the word)
                         const float x0 = to_f32(a[i].e[2 * u]), x1 = to_f32(a[i].e[2 * u + 1]);
                         from_f32(a[i].e[2 * u], x0 * c[u] - x1 * s[u]);
                         from_f32(a[i].e[2 * u + 1], x1 * c[u] + x0 * s[u]);
                     }
-                } else {
+                } else if (pair) {
 #pragma unroll
-                    for (int u = 0; u < V; ++u) {
+                    for (int u = 0; u < kVec; ++u) {
                         const float x0 = to_f32(a[i].e[u]), x1 = to_f32(b[i].e[u]);
                         from_f32(a[i].e[u], x0 * c[u] - x1 * s[u]);
                         from_f32(b[i].e[u], x1 * c[u] + x0 * s[u]);
                     }
                 }
             }
-            T* dst = target(r);
-            *reinterpret_cast<decltype(a[i].w)*>(dst + e0) = a[i].w;
-            if (pair) *reinterpret_cast<decltype(a[i].w)*>(dst + e1) = b[i].w;
+            T* dst = rows_of.target(r, slot);
+            *reinterpret_cast<uint4*>(dst + e0) = a[i].w;
+            if (pair) *reinterpret_cast<uint4*>(dst + e1) = b[i].w;
         }
     }
 }
 
-template <typename T, bool kInterleaved, int V>
+// The half layout where R / 2 is not a multiple of 8: a word's partners straddle
+// two words.  The rows go through shared memory as well; a thread turns the same
+// word of several rows, taking its partners (element e pairs with e + R / 2 or
+// e - R / 2) one by one from there.  (Moving such rows by 2-byte
+// elements took 105 us where this takes 67 us: 16384 tokens of 8q/8kv heads
+// of 128, R = 90.)
+constexpr int kStagedThreads = 128;
+constexpr int kStagedBatch = 3;    // head rows a thread turns between two barriers
+
+template <typename T>
+__global__ void __launch_bounds__(kStagedThreads, 10) rope_write_staged_kernel(const RopeParams p) {
+    __shared__ float sm_cos[kRopeMaxDim / 2], sm_sin[kRopeMaxDim / 2];
+    __shared__ __align__(16) T sm_rows[kStagedBatch * kStagedThreads * kVec];
+    const int t = blockIdx.x, tid = threadIdx.y * blockDim.x + threadIdx.x;
+    const TokenRows<T> rows_of = {p, t};
+    const int D = p.head_dim, R = p.rotary_dim, half = R / 2;
+    const int rotated_rows = p.num_q_heads + p.num_kv_heads;
+    const int rows = rotated_rows + p.num_kv_heads;
+    const int e0 = threadIdx.x * kVec, step = kStagedBatch * (int)blockDim.y;
+    uint4 a[kStagedBatch];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kStagedBatch; ++i) {
+            const int r = r0 + threadIdx.y + i * blockDim.y;
+            if (r < rows) a[i] = *reinterpret_cast<const uint4*>(rows_of.source(r) + e0);
+        }
+    };
+    load(0);  // (a padding token's rows are there too)
+    int pos = 0;
+    int64_t slot;
+    if (!token_place(p, t, tid == 0, pos, slot)) return;  // uniform over the CTA
+    for (int j = tid; j < half; j += blockDim.x * blockDim.y)
+        rotation(pos, p.inv_freq[j], p.rope_scale, sm_cos[j], sm_sin[j]);
+    __syncthreads();
+    // this thread's elements, the same in every row: those before `half` pair
+    // with e + half (y0 = x0 c - x1 s), the others with e - half (y1 = x1 c + x0 s)
+    const int firsts = half - e0;  // how many are
+    float c[kVec], sn[kVec];
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+        const int e = min(e0 + u, R - 1), j = e < half ? e : e - half;
+        c[u] = sm_cos[j];
+        sn[u] = u < firsts ? -sm_sin[j] : sm_sin[j];
+    }
+    for (int r0 = 0; r0 < rows; r0 += step) {
+        if (r0 > 0) {
+            load(r0);
+            __syncthreads();  // the last rows have been read
+        }
+#pragma unroll
+        for (int i = 0; i < kStagedBatch; ++i)
+            if (r0 + (int)threadIdx.y + i * (int)blockDim.y < rows)
+                *reinterpret_cast<uint4*>(sm_rows + (threadIdx.y + i * blockDim.y) * D + e0) = a[i];
+        __syncthreads();
+#pragma unroll 1
+        for (int i = 0; i < kStagedBatch; ++i) {
+            const int k = threadIdx.y + i * blockDim.y, r = r0 + k;
+            if (r >= rows) break;
+            const T* row = sm_rows + k * D;
+            Vec<T> x;
+            x.w = *reinterpret_cast<const uint4*>(row + e0);
+            if (r < rotated_rows && e0 < R) {
+#pragma unroll
+                for (int u = 0; u < kVec; ++u) {
+                    if (e0 + u >= R) continue;
+                    const float y = to_f32(row[e0 + u + (u < firsts ? half : -half)]);
+                    from_f32(x.e[u], to_f32(x.e[u]) * c[u] + y * sn[u]);
+                }
+            }
+            *reinterpret_cast<uint4*>(rows_of.target(r, slot) + e0) = x.w;
+        }
+    }
+}
+
+template <typename T, bool kInterleaved>
 pkv_status launch_rope(const RopeParams& p, cudaStream_t stream) {
-    const int R = p.rotary_dim;
-    const int units = (kInterleaved ? R : R / 2) / V + (p.head_dim - R) / V;  // of a head row
+    // units of a head row, and rows of threads
+    const int units = (p.head_dim - (kInterleaved ? 0 : p.rotary_dim / 2)) / kVec;
     const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-    int y = kRopeThreads / units;
-    if (y > rows) y = rows;
-    if (y < 1) y = 1;
-    rope_write_kernel<T, kInterleaved, V>
+    // CTAs of 128 threads; 64 where a token has little and there are many tokens
+    // (16384 tokens of 24 rows of 128: 33.4 us with 64, 35.6 with 128; of 48 rows
+    // 61.3 and 60.0; four tokens 3.5 and 2.7)
+    const bool little = rows * p.head_dim * 2 < 8192 && p.num_tokens >= 4096;
+    const int threads = little ? kRopeThreads / 2 : kRopeThreads;
+    const int y = std::max(1, std::min(rows, threads / units));
+    rope_write_kernel<T, kInterleaved>
         <<<p.num_tokens, dim3((unsigned)units, (unsigned)y), 0, stream>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
-// The widest vector that divides the rotated part's runs.
 template <typename T>
 pkv_status dispatch_rope(const RopeParams& p, bool interleaved, cudaStream_t stream) {
-    const int run = interleaved ? p.rotary_dim : p.rotary_dim / 2;
-    if (interleaved) {
-        if (run % 8 == 0) return launch_rope<T, true, 8>(p, stream);
-        if (run % 4 == 0) return launch_rope<T, true, 4>(p, stream);
-        return launch_rope<T, true, 2>(p, stream);
-    }
-    if (run % 8 == 0) return launch_rope<T, false, 8>(p, stream);
-    if (run % 4 == 0) return launch_rope<T, false, 4>(p, stream);
-    if (run % 2 == 0) return launch_rope<T, false, 2>(p, stream);
-    return launch_rope<T, false, 1>(p, stream);
+    if (interleaved) return launch_rope<T, true>(p, stream);
+    if (p.rotary_dim / 2 % kVec == 0) return launch_rope<T, false>(p, stream);
+    const int words = p.head_dim / kVec, rows = p.num_q_heads + 2 * p.num_kv_heads;
+    const int y = std::max(1, std::min(rows, kStagedThreads / words));
+    rope_write_staged_kernel<T>
+        <<<p.num_tokens, dim3((unsigned)words, (unsigned)y), 0, stream>>>(p);
+    return cuda_status(cudaGetLastError());
 }
 
 pkv_status rope_impl(RopeParams& p, int layout, pkv_dtype dtype, pkv_stream_t stream) {
