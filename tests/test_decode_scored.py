@@ -200,6 +200,39 @@ def test_batches(cuda_device, B, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hkv,D,window", [(8, 128, 0), (8, 64, 0), (3, 64, 20000)])
+def test_long_batches(cuda_device, Hkv, D, window):
+    """Long contexts in a batch, several sequences to a warp's run and several warps
+    to a sequence: checked on some sequences, and the same from call to call."""
+    B, g = 26 if Hkv == 8 else 40, 2
+    lens = [40000 - 531 * i for i in range(B)]
+    dev = cuda_device
+    gen = torch.Generator(device=dev).manual_seed(5)
+    need = [(n + BS - 1) // BS for n in lens]
+    NB = sum(need)
+    tables, at = [], 0
+    perm = torch.randperm(NB, generator=gen, device=dev).tolist()
+    for x in need:
+        tables.append(perm[at:at + x] + [0] * (max(need) - x))
+        at += x
+    mk = lambda *s: torch.randn(*s, generator=gen, device=dev, dtype=torch.float32).to(f16)
+    kc, vc = (torch.empty(NB, BS, Hkv, D, dtype=f16, device=dev) for _ in range(2))
+    for i in range(0, NB, 4096):
+        m = min(4096, NB - i)
+        kc[i:i + m], vc[i:i + m] = mk(m, BS, Hkv, D), mk(m, BS, Hkv, D)
+    inp = dict(q=mk(B, Hkv * g, D), k_cache=kc, v_cache=vc, tables=tables, lens=lens, starts=None,
+               window=window)
+    ws = pkv.new_scored_workspace(B, Hkv * g, Hkv, D, 40000, dev).fill_(255)
+    out = run(inp, 40000, D ** -0.5, softcap=30.0, ws=ws)
+    for s in (0, 1, B // 2, B - 1):
+        want, tol = attention(inp["q"][s:s + 1], kc, vc, [tables[s]], [lens[s]], None, D ** -0.5,
+                              softcap=30.0, window=window)
+        assert_close(out[s:s + 1], want, tol)
+    for _ in range(4):
+        assert torch.equal(run(inp, 40000, D ** -0.5, softcap=30.0, ws=ws), out)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale,cap,q_std", [(1.0, 0.0, 30.0), (1.0, 50.0, 30.0), (-0.5, 8.0, 2.0),
                                              (0.0, 0.0, 1.0), (0.1, 1e6, 2.0), (0.1, 0.01, 2.0),
                                              (1e-4, 300.0, 1.0)])
