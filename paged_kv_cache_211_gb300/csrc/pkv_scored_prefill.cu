@@ -276,6 +276,19 @@ __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t (&w)[8]) 
                  : "memory");
 }
 
+// A pair of 16-bit values times a power of two.
+template <typename T>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t x, float f) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&x), __float2half2_rn(f));
+        return *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+        const __nv_bfloat162 y =
+            __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), __float2bfloat162_rn(f));
+        return *reinterpret_cast<const uint32_t*>(&y);
+    }
+}
+
 // One lane of a converged warp (1 there, 0 elsewhere).
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t one;
@@ -822,6 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float f = 1.f;  // factor on what the row has so far
                 // sc becomes z / mul (z: base-2 scores), with mul > 0
                 float mul = md.scale_log2, ms = 0.f;
+                float m_mine = 0.f, down = 1.f;
                 bool done = false;
                 if constexpr (kCap) {
                     const float top = largest(sc);
@@ -904,22 +918,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < kHalf; c += 2)
                             mxp[(c >> 1) & 3] = max3(mxp[(c >> 1) & 3], sc[c], sc[c + 1]);
-                        float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mul;
-                        // the row's maximum over both halves
-                        float* mine = xm + (((tiles & 1) * 2 + X) * 2 + q) * kRows + r;
-                        *mine = mx;
+                        const float mx =
+                            fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * mul;
+                        // The reference 2^m of the weights is a whole power, and follows
+                        // the row's maximum only where that grew by more than 2^kRescale.
+                        // This half tells the other what it wants, takes its own for the
+                        // weights meanwhile, and scales them after if the other's is larger
+                        // (by a power of two: exact).
+                        m_mine = m_used == -INFINITY || mx > m_used + kRescale ? ceilf(mx) : m_used;
+                        xm[(((tiles & 1) * 2 + X) * 2 + q) * kRows + r] = m_mine;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&x_max[4 * X + wq]);
+                        ms = m_mine == -INFINITY ? 0.f : m_mine;
+                    }
+                    // P as 16-bit pairs; the sum takes the unrounded weights
+                    const uint64_t mul2 = f2(mul, mul), nms2 = f2(-ms, -ms);
+                    uint32_t pk[kHalf / 2];
+#pragma unroll
+                    for (int e = 0; e < kHalf / 2; ++e) {
+                        float a0 = sc[2 * e], a1 = sc[2 * e + 1];
+                        if constexpr (!kFixed) f2_split(f2_fma(f2(a0, a1), mul2, nms2), a0, a1);
+                        const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                        acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
+                        pk[e] = E::pack(p0, p1);
+                    }
+                    if constexpr (!kFixed) {
                         ok = __all_sync(0xffffffffu, mbar_wait(&x_max[4 * X + wq], tiles & 1,
                                                                abort_flag, p.status));
                         if (!ok) break;
-                        mx = fmaxf(mx, *(mine + (q ? -kRows : kRows)));
-                        const float m_new = fmaxf(m_used, mx);
-                        // lazy rescale: only when the maximum grew by more than 2^kRescale
-                        const bool grow = m_used != -INFINITY && m_new > m_used + kRescale;
+                        const float m_new = fmaxf(
+                            m_mine, xm[(((tiles & 1) * 2 + X) * 2 + (q ^ 1)) * kRows + r]);
+                        const bool grow = m_used != -INFINITY && m_new > m_used;
                         f = grow ? fast_exp2(m_used - m_new) : 1.f;
-                        if (m_used == -INFINITY || grow) m_used = m_new;
-                        ms = m_used == -INFINITY ? 0.f : m_used;
+                        const bool low = m_new > m_mine;
+                        m_used = m_new;
+                        if (__any_sync(0xffffffffu, low)) {
+                            // (below 2^-24 of the other half's largest weight: nothing)
+                            down = low ? fast_exp2(m_mine - m_new) : 1.f;
+#pragma unroll
+                            for (int e = 0; e < kHalf / 2; ++e) pk[e] = scale_pair<T>(pk[e], down);
+                        }
                         if (__any_sync(0xffffffffu, grow)) {  // (the same in both halves' warps)
                             // S_X(J) was issued after P V_X(J-1): O_X holds every earlier tile
 #pragma unroll 1
@@ -944,22 +982,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ++rescales;
                         }
                     }
-                    // P as 16-bit pairs (every score is in registers); the sum takes
-                    // the unrounded weights
-                    const uint64_t mul2 = f2(mul, mul), nms2 = f2(-ms, -ms);
-#pragma unroll
-                    for (int w = 0; w < kHalf / 32; ++w) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float a0 = sc[32 * w + 2 * e], a1 = sc[32 * w + 2 * e + 1];
-                            if constexpr (!kFixed) f2_split(f2_fma(f2(a0, a1), mul2, nms2), a0, a1);
-                            const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-                            acc2[e & 3] = f2_add(acc2[e & 3], f2(p0, p1));
-                            pk[e] = E::pack(p0, p1);
-                        }
-                        tc_st16(sx + 16 * w, pk);
-                    }
+                    tc_st16(sx, reinterpret_cast<uint32_t(&)[16]>(pk[0]));
+                    tc_st16(sx + 16, reinterpret_cast<uint32_t(&)[16]>(pk[16]));
                 }
                 tc_wait_st();
                 // V rows that no row of the item sees (or that were not loaded)
@@ -985,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     f2_split(acc2[e], a0, a1);
                     psum += a0 + a1;
                 }
-                l = l * f + psum;
+                l = l * f + psum * down;
             }
             if (!ok) break;
             // ---- epilogue: O_X / l (this half's columns) for the rows of the chunk,
