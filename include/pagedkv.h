@@ -457,6 +457,10 @@ pkv_status paged_kv_rope_write_new_tokens(
  * Only table entries of blocks with a key some query of the sequence sees are
  * read, so blocks that slid out of the window may have been freed.  K and V of
  * keys that a query does not see never reach its output, NaN included.
+ * out must share no byte with q (PKV_ERR_INVALID_ARG).  Equal calls give equal
+ * bits: nothing depends on the order in which the GPU's SMs come to their work.
+ * The decode kernels and the prefill's second one are programmatic dependents
+ * and let their own dependents be scheduled early, under the rules above.
  * ------------------------------------------------------------------------- */
 size_t paged_attention_decode_scored_workspace_bytes(int num_seqs, int num_q_heads,
                                                      int num_kv_heads, int head_dim,

@@ -56,6 +56,12 @@ __device__ __forceinline__ int first_key(const ScoreMods& m, int s, int p) {
     return lo;
 }
 
+// Whether two buffers of `bytes` bytes share any.
+inline bool overlap(const void* a, const void* b, size_t bytes) {
+    const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bytes && y < x + bytes;
+}
+
 // Host checks shared by the entries.  false: invalid argument.
 inline bool make_score_mods(ScoreMods* m, float scale, float softcap, const float* alibi_slopes,
                             int window, const int32_t* key_starts, const int32_t* prefix_lens) {

@@ -566,7 +566,11 @@ __global__ void __launch_bounds__(HPS * (D / 16) * 32)
     const int HG = num_q_heads / g / HPS;
     for (int row = blockIdx.x; row < num_rows; row += gridDim.x) {
         const RowParts d = rows[row];
-        if (d.first == d.last) continue;
+        // (a call whose waits gave up may leave anything here: nothing out of range
+        // is taken for a part)
+        if (d.first >= d.last || d.first < 0 || d.last >= kMaxCtas * kWarps ||
+            d.first_slot >> 1 != d.first)
+            continue;
         auto slot_of = [&](int c) { return c == d.first ? d.first_slot : 2 * c; };
         auto ml_of = [&](int c) {  // m, l of heads 2 tig and 2 tig + 1
             return *reinterpret_cast<const float4*>(ml + ((size_t)slot_of(c) * HPS + e) * kMaxGroup +
@@ -741,6 +745,8 @@ pkv_status paged_attention_decode_scored(
         return PKV_ERR_INVALID_ARG;
     if (!pkv::aligned16(q) || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache) ||
         !pkv::aligned16(out))
+        return PKV_ERR_INVALID_ARG;
+    if (pkv::overlap(q, out, (size_t)num_seqs * num_q_heads * head_dim * 2))
         return PKV_ERR_INVALID_ARG;
     const size_t need = paged_attention_decode_scored_workspace_bytes(
         num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len);

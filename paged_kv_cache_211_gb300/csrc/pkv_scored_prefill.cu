@@ -1194,6 +1194,24 @@ Workspace ws_layout(long long rows, int head_dim) {
     return w;
 }
 
+// The fewer terms of tanh(x) / x = 1 - x^2 / 3 + 2 x^4 / 15 - ... for small x
+// (what is left out is below 4e-7 there).
+constexpr float kTanhSmall[3][3] = {{1.f, 0.f, 0.f}, {1.f, -0.333333333f, 0.f},
+                                    {kTanh3[0], kTanh3[1], kTanh3[2]}};
+constexpr float kTanhSmallRange[3] = {1e-3f, 0.04f, kTanhFewRange};
+
+// The terms c_i x^2i as terms of (raw score)^2i times the cap's scale; returns
+// `range`, or -1 if one of them leaves the normal numbers.
+float scaled_terms(const float* c, int n, float range, const ScoreMods& m, float* out) {
+    const double c2 = (double)m.cap_in * m.cap_in;
+    double f = m.scale_log2;
+    for (int i = 0; i < n; ++i, f *= c2) {
+        out[i] = (float)(c[i] * f);
+        if (!std::isnormal(out[i])) return -1.f;
+    }
+    return range;
+}
+
 template <int D>
 size_t prefill_smem() {
     // 2 Q tiles, 2 K and 2 V stages, barriers (under 1 KB) and the halves'
@@ -1296,6 +1314,8 @@ pkv_status paged_attention_prefill_scored(
     if (!pkv::aligned16(q) || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache) ||
         !pkv::aligned16(out))
         return PKV_ERR_INVALID_ARG;
+    if (pkv::overlap(q, out, (size_t)num_q_rows * num_q_heads * head_dim * 2))
+        return PKV_ERR_INVALID_ARG;
     const size_t need = paged_attention_prefill_scored_workspace_bytes(
         num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim);
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
@@ -1335,19 +1355,21 @@ pkv_status paged_attention_prefill_scored(
     // z = cap' x (tanh(x) / x) with x = raw cap_in: the terms in raw^2, times cap' cap_in
     prm.tanh_limit = prm.tanh_few_limit = -1.f;
     if (softcap > 0.f && scale != 0.f) {
-        const double c2 = (double)prm.mods.cap_in * prm.mods.cap_in;
-        double f = prm.mods.scale_log2;
-        bool ok = true;
-        for (int i = 0; i < pkv::kTanhTerms; ++i, f *= c2) {
-            prm.tanh_z[i] = (float)(pkv::kTanh4[i] * f);
-            ok = ok && std::isnormal(prm.tanh_z[i]);
-            if (i < pkv::kTanhFew) prm.tanh_few[i] = (float)(pkv::kTanh3[i] * f);
+        const float in = std::fabs(prm.mods.cap_in);
+        float range = pkv::scaled_terms(pkv::kTanh4, pkv::kTanhTerms, pkv::kTanhRange, prm.mods,
+                                        prm.tanh_z);
+        // caps far above the scores: the last terms leave the range of fp32, and
+        // are not needed where x is small enough
+        for (int n = pkv::kTanhTerms - 1; range < 0.f && n > 0; --n) {
+            for (float& t : prm.tanh_z) t = 0.f;
+            range = pkv::scaled_terms(pkv::kTanhSmall[n - 1], n, pkv::kTanhSmallRange[n - 1],
+                                      prm.mods, prm.tanh_z);
         }
-        const float limit = pkv::kTanhRange / std::fabs(prm.mods.cap_in);
-        if (ok && limit < 1e18f) {  // (its square is finite)
-            prm.tanh_limit = limit;
-            prm.tanh_few_limit = pkv::kTanhFewRange / std::fabs(prm.mods.cap_in);
-        }
+        // (raw^2 has to be finite as well)
+        if (range > 0.f) prm.tanh_limit = std::min(range / in, 1e18f);
+        const float few = pkv::scaled_terms(pkv::kTanh3, pkv::kTanhFew, pkv::kTanhFewRange,
+                                            prm.mods, prm.tanh_few);
+        if (few > 0.f) prm.tanh_few_limit = std::min(few / in, 1e18f);
     }
     const pkv::Workspace ws =
         pkv::ws_layout(pl.splits > 1 ? pl.items * pl.splits * pkv::kPair : 0, head_dim);

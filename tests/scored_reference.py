@@ -16,7 +16,9 @@ def attention(q, k_cache, v_cache, tables, lens, chunks, scale, softcap=0.0, slo
     not, so sum w |V| e; the result's rounding is e |out|.  A score's fp32 error
     d shifts weights by at most 2 d relative: the dot product's D / 16 partial
     accumulations lose at most 2^-22 of sum |q k| each (2^-19 in all), and the
-    cap, bias, scaling and exponent round to 2^-21 of their largest operand.
+    cap, bias, scaling and exponent round to 2^-21 of their largest operand (the
+    cap itself only where some score of the sequence comes near it: elsewhere
+    tanh is taken to a relative error).
     exp2 and the running sums add 2^-18.  fp16 weights below 2^-14 are off by up
     to 2^-25 of the largest one: 2^-25 max(w) sum |V|.
     """
@@ -53,6 +55,14 @@ def attention(q, k_cache, v_cache, tables, lens, chunks, scale, softcap=0.0, slo
         seen, t = seen[:, first:], t[first:]
         if t.numel() == 0:
             continue
+        near_cap = 0.0
+        for h in range(Hq if softcap else 0):
+            Kh = torch.where(any_row[first:, None], K[:, h // g], torch.zeros((), dtype=f64, device=dev))
+            z = (scale * (q[rows, h].to(f64) @ Kh.T)).abs()
+            if bool((torch.where(torch.isnan(z), torch.full_like(z, float("inf")), z)
+                     > softcap / 5).any()):
+                near_cap = softcap
+                break
         for h in range(Hq):
             qh = q[rows, h].to(f64)
             Kh = torch.where(any_row[first:, None], K[:, h // g], torch.zeros((), dtype=f64, device=dev))
@@ -83,7 +93,7 @@ def attention(q, k_cache, v_cache, tables, lens, chunks, scale, softcap=0.0, slo
             a = mix(w, Vh.abs())
             d = 2.0 ** -19 * torch.where(seen, size, torch.zeros_like(size)).amax(1, keepdim=True)
             d = d + 2.0 ** -21 * (torch.where(seen, big, torch.zeros_like(big)).amax(1, keepdim=True)
-                                  + abs(softcap))
+                                  + near_cap)
             small = 2.0 ** -25 * w.amax(1, keepdim=True) * (
                 seen.to(f64) @ torch.where(torch.isfinite(Vh), Vh.abs(), torch.zeros_like(Vh))
             ) if dt == torch.float16 else 0.0

@@ -61,6 +61,7 @@ def _c_call(**over):
     (dict(max_blocks_per_seq=1 << 27), 2), (dict(num_blocks=1 << 27), 2),
     (dict(workspace=None), 6), (dict(workspace_bytes=1000), 6), (dict(workspace=(7 << 20) + 16), 6),
     (dict(num_seqs=0), 0), (dict(num_seqs=0, q=None, workspace=None), 0),
+    (dict(out=1 << 20), 1), (dict(out=(1 << 20) + 2032), 1), (dict(out=(1 << 20) - 2032), 1),
 ])
 def test_decode_scored_c_statuses(over, status):
     assert _c_call(**over) == status
@@ -234,7 +235,8 @@ def test_long_batches(cuda_device, Hkv, D, window):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("scale,cap,q_std", [(1.0, 0.0, 30.0), (1.0, 50.0, 30.0), (-0.5, 8.0, 2.0),
-                                             (0.0, 0.0, 1.0), (0.1, 1e6, 2.0), (0.1, 0.01, 2.0),
+                                             (0.0, 0.0, 1.0), (0.1, 1e3, 2.0), (0.1, 1e6, 2.0),
+                                             (0.1, 1e9, 2.0), (0.1, 1e15, 2.0), (0.1, 0.01, 2.0),
                                              (1e-4, 300.0, 1.0)])
 def test_extreme_scores(cuda_device, scale, cap, q_std):
     inp = make(cuda_device, [1, 50, 700], 8, 2, 128, bf, seed=9, q_std=q_std)

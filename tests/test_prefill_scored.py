@@ -62,6 +62,7 @@ def _c_call(**over):
     (dict(max_blocks_per_seq=1 << 27), 2), (dict(num_blocks=1 << 27), 2),
     (dict(workspace=None), 6), (dict(workspace_bytes=100), 6), (dict(workspace=(8 << 20) + 128), 6),
     (dict(num_seqs=0), 0), (dict(max_q_len=0, q=None), 0), (dict(num_q_rows=0, workspace=None), 0),
+    (dict(out=1 << 20), 1), (dict(out=(1 << 20) + 12272), 1), (dict(out=(1 << 20) - 12272), 1),
 ])
 def test_prefill_scored_c_statuses(over, status):
     assert _c_call(**over) == status
@@ -224,7 +225,8 @@ def test_documents_share_one_cached_sequence(cuda_device):
 @pytest.mark.gpu
 @pytest.mark.parametrize("scale,cap,q_std", [(1.0, 0.0, 30.0), (1.0, 50.0, 30.0), (-0.5, 8.0, 2.0),
                                              (-0.1, 0.0, 2.0), (0.0, 0.0, 1.0), (0.0, 4.0, 1.0),
-                                             (0.1, 1e6, 2.0), (0.1, 0.01, 2.0), (1e-4, 300.0, 1.0)])
+                                             (0.1, 1e3, 2.0), (0.1, 1e6, 2.0), (0.1, 1e9, 2.0),
+                                             (0.1, 1e15, 2.0), (0.1, 0.01, 2.0), (1e-4, 300.0, 1.0)])
 def test_extreme_scores(cuda_device, scale, cap, q_std):
     inp = make(cuda_device, [100, 30], [100, 700], 8, 2, 128, bf, seed=9, q_std=q_std)
     check(inp, scale, softcap=cap)
@@ -332,6 +334,24 @@ def test_graph_replay_on_another_stream(cuda_device, chunks, lens):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first) and pkv.pkv_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [f16, bf])
+@pytest.mark.parametrize("cap", [0.0, 25.0])
+def test_ragged_chunks_repeat_bit_for_bit(cuda_device, dtype, cap):
+    """Items with and without a second tile in every order, sorted and dealt: equal
+    calls give equal bits, and the bits of the definition's bound."""
+    gen = torch.Generator().manual_seed(3)
+    chunks = [int(x) for x in torch.randint(1, 420, (40,), generator=gen)]
+    lens = [c + int(x) for c, x in zip(chunks, torch.randint(0, 900, (40,), generator=gen))]
+    inp = make(cuda_device, chunks, lens, 10, 5, 128, dtype, seed=12, q_std=4.0)
+    out = run(inp, 0.1, softcap=cap)
+    for _ in range(15):
+        assert torch.equal(run(inp, 0.1, softcap=cap), out)
+    want, tol = attention(inp["q"], inp["k_cache"], inp["v_cache"], inp["tables"], lens, chunks,
+                          0.1, cap)
+    assert_close(out, want, tol)
 
 
 @pytest.mark.gpu
