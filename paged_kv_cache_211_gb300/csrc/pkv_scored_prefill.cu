@@ -423,7 +423,7 @@ __device__ __noinline__ void redo_rows(const PrefillScored& p, Item it, int row0
 
 // Raw scores to capped base-2 scores z = cap' tanh(raw cap_in), cap' = cap
 // log2(e).  Where the whole warp's scores allow it z is raw times a polynomial
-// in raw^2, two scores an instruction; else cap' - 2 cap' / (1 + e^2x).
+// in raw^2, two scores an instruction; else cap_score.
 // top: the largest |raw score|.
 __device__ __forceinline__ float largest(const float (&sc)[kHalf]) {
     float top[4] = {0.f, 0.f, 0.f, 0.f};
@@ -455,11 +455,10 @@ __device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[kHa
                 f2_split(f2_mul(x[u], y[u]), sc[e0 + 2 * u], sc[e0 + 2 * u + 1]);
         }
     } else {
-        const float k2 = 2.f * kScoreLog2e * p.mods.cap_in;
-        const float cap = p.mods.cap_out;
+        // score by score: one large score (a hidden one's leftovers in shared memory
+        // even) must not cost its neighbours near zero their relative error
 #pragma unroll
-        for (int c = 0; c < kHalf; ++c)
-            sc[c] = fmaf(-2.f * cap, fast_rcp(1.f + fast_exp2(k2 * sc[c])), cap);
+        for (int c = 0; c < kHalf; ++c) sc[c] = cap_score(sc[c], p.mods);
     }
 }
 

@@ -233,6 +233,22 @@ def test_extreme_scores(cuda_device, scale, cap, q_std):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,scale,cap", [(bf, 0.1, 1e6), (f16, 0.1, 1e5), (bf, 0.1, 50.0)])
+@pytest.mark.parametrize("reps", [1, 30])
+def test_large_scores_leave_small_ones_exact(cuda_device, dtype, scale, cap, reps):
+    """Rows whose scores reach the cap beside rows whose scores are far below it, after
+    a call that left huge values wherever the kernel keeps its tiles."""
+    dev = cuda_device
+    big = make(dev, [200] * 40, [300] * 40, 4, 2, 128, dtype, seed=1)
+    big["k_cache"].fill_(3e4)
+    big["v_cache"].fill_(-3e4)
+    inp = make(dev, [100, 30] * reps, [100, 700] * reps, 8, 2, 128, dtype, seed=9, q_std=2.0)
+    inp["q"][5::16] *= 0.9 * cap / (scale * 30.0) if cap < 1e3 else 2.0 ** 9
+    run(big, 1.0, softcap=1e6)
+    check(inp, scale, softcap=cap)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("reps", [1, 24])
 def test_hidden_values_never_reach_a_row(cuda_device, reps):
     """Infinities and NaN in K and V of keys that some rows see and others do not:
