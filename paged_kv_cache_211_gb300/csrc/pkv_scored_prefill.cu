@@ -432,6 +432,7 @@ __device__ __forceinline__ float largest(const float (&sc)[kHalf]) {
         top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], fabsf(sc[c]), fabsf(sc[c + 1]));
     return max3(fmaxf(top[0], top[1]), top[2], top[3]);
 }
+template <bool kSmallCap>
 __device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[kHalf], float top) {
     if (__all_sync(0xffffffffu, top <= p.tanh_limit)) {
         const uint64_t c3 = f2(p.tanh_z[3], p.tanh_z[3]), c2 = f2(p.tanh_z[2], p.tanh_z[2]);
@@ -456,9 +457,16 @@ __device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[kHa
         }
     } else {
         // score by score: one large score (a hidden one's leftovers in shared memory
-        // even) must not cost its neighbours near zero their relative error
+        // even) must not cost its neighbours near zero their relative error.  Under
+        // a small cap (kSmallCap: cap' <= kFixedMax) the far form alone is within
+        // 2^-16 of every z, and shorter.
 #pragma unroll
-        for (int c = 0; c < kHalf; ++c) sc[c] = cap_score(sc[c], p.mods);
+        for (int c = 0; c < kHalf; ++c)
+            sc[c] = kSmallCap ? fmaf(-2.f * p.mods.cap_out,
+                                     fast_rcp(1.f + fast_exp2(2.f * kScoreLog2e * p.mods.cap_in *
+                                                              sc[c])),
+                                     p.mods.cap_out)
+                              : cap_score(sc[c], p.mods);
     }
 }
 
@@ -883,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         done = true;
                     } else {
-                        cap_to_z(p, sc, top);
+                        cap_to_z<kFixed>(p, sc, top);
                     }
                 }
                 if (!done) {
