@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // whole warpgroups: warps 0-3 release registers, 4-11 take them
+    // whole warpgroups: warps 0-3 release registers, 4-19 take them
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp == 0 || warp == 3) {
@@ -583,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int rd = 0; rd < rounds && live; ++rd) {
             Item it;
             if (!round_at(p, table, num_items, rd, isk && lane == 0, it)) continue;
-            const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks_per_seq + it.b0;
+            const int32_t* blocks =
+                p.block_tables + (size_t)it.s * p.max_blocks_per_seq + it.b0;
             for (int j = 0; j < it.nkv; ++j, ++J) {
                 const int b = J & 1, ph = (J >> 1) & 1;
                 live = __all_sync(0xffffffffu, mbar_wait(&empty[b], ph ^ 1, abort_flag, p.status));
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int id = 0;
                 bool bad = false;
                 if (lane < nb) {
-                    id = table[kTileBlocks * j + lane];
+                    id = blocks[kTileBlocks * j + lane];
                     bad = id < 0 || id >= p.num_blocks;
                     if (bad) id = 0;  // fetched, then masked and zeroed
                 }
