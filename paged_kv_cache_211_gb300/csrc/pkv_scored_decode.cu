@@ -32,7 +32,7 @@
 // Measured: 32 sequences of 2048 to 32768 tokens, 32q/8kv heads of 128, bf16,
 // cap 50: 181 us, 6.2 TB/s of K and V (the first kernel alone 6.5 TB/s); a
 // 1000-token window over 256 sequences, 32q/4kv heads of 64: 50 us, 5.0 TB/s; 60
-// sequences of 32 to 512 tokens, 16q/8kv heads of 128: 14.5 us, of which the
+// sequences of 32 to 512 tokens, 16q/8kv heads of 128: 14.2 us, of which the
 // launch, the lengths and the first copies take 6 and the join 4.  Equal runs end
 // up to a tenth apart, by SM; handing their last eighth out as chunks made them
 // end together but no sooner (HBM is busy until the first ones end), and its
@@ -49,7 +49,7 @@ constexpr int kMaxCtas = 160;     // bounds the workspace: persistent CTAs, one 
 constexpr int kMaxSeqs = 8192;    // per call (lengths and offsets live in shared memory)
 constexpr int kMaxGroup = 8;      // query heads per KV head: the n side of the MMA
 constexpr int kMaxStages = 3;     // stages of 8 KB per warp
-constexpr int kMinUnits = 2;      // shortest run worth a warp of its own
+constexpr int kMinUnits = 4;      // shortest run worth a warp of its own
 constexpr int kRowBlocks = 8;     // longest row (blocks) that a warp takes whole
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -558,87 +558,118 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the rows that several workers share, a row per CTA and
-// round; warp (e, i) has fragment i of head e from every part.
-constexpr int kFewParts = 6;
+// round.  Warp (u, e, i) has fragment i of head e from every kTeams-th part,
+// kBatch of them in flight at a time, with a running maximum; the kTeams teams
+// meet in shared memory.  Few rows have many parts each and take four teams:
+// with one team, and the maxima in a pass of their own, two rows of 47 parts took
+// 19.4 us in all and one of 346 took 28.5 where these take 11.6 and 13.3.  Many
+// rows have a few parts each: with four teams 496 rows take 19.9 us, with one 14.2.
+constexpr int kBatch = 4;
 constexpr int kJoinCtas = 4 * kMaxCtas;
+constexpr int kManyTeams = 4, kManyTeamRows = 256;
 
-template <typename T, int D, int HPS>
-__global__ void __launch_bounds__(HPS * (D / 16) * 32)
+template <typename T, int D, int HPS, int kTeams>
+__global__ void __launch_bounds__(kTeams * HPS * (D / 16) * 32)
     scored_join_kernel(const RowParts* __restrict__ rows, const float2* __restrict__ ml,
                        const float4* __restrict__ o, void* out, int num_rows, int num_q_heads,
                        int g) {
-    constexpr int KS = D / 16;
+    constexpr int KS = D / 16, F = HPS * KS;
+    __shared__ float4 sm_ml[kTeams > 1 ? kTeams * F * 32 : 1];   // m, l of the lane's two heads
+    __shared__ float4 sm_acc[kTeams > 1 ? kTeams * F * 32 : 1];
     // the next kernel's CTAs may be scheduled beside these; it waits for this
     // grid before it touches anything (griddepcontrol.wait)
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    const int e = (threadIdx.x >> 5) / KS, i = (threadIdx.x >> 5) % KS;
+    const int lane = threadIdx.x & 31, tig = lane & 3;
+    const int warp = threadIdx.x >> 5, team = warp / F, f = warp - team * F;
+    const int e = f / KS, i = f - e * KS;
     const bool has = 2 * tig < g;
     const int HG = num_q_heads / g / HPS;
-    for (int row = blockIdx.x; row < num_rows; row += gridDim.x) {
-        const RowParts d = rows[row];
+    // 32 rows' descriptions at a time
+    for (long long r0 = blockIdx.x; r0 < num_rows; r0 += 32ll * gridDim.x) {
+        const long long r = r0 + (long long)lane * gridDim.x;
+        RowParts mine = {};
+        if (r < num_rows) mine = rows[r];
         // (a call whose waits gave up may leave anything here: nothing out of range
         // is taken for a part)
-        if (d.first >= d.last || d.first < 0 || d.last >= kMaxCtas * kWarps ||
-            d.first_slot >> 1 != d.first)
-            continue;
-        auto slot_of = [&](int c) { return c == d.first ? d.first_slot : 2 * c; };
-        auto ml_of = [&](int c) {  // m, l of heads 2 tig and 2 tig + 1
-            return *reinterpret_cast<const float4*>(ml + ((size_t)slot_of(c) * HPS + e) * kMaxGroup +
-                                                    2 * tig);
-        };
-        auto o_of = [&](int c) { return o[(((size_t)slot_of(c) * HPS + e) * KS + i) * 32 + lane]; };
-        float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](const float4& v, const float4& x) {
-            const float w0 = fast_exp2(v.x - M0), w1 = fast_exp2(v.z - M1);
-            L0 += w0 * v.y;
-            L1 += w1 * v.w;
-            acc.x += w0 * x.x;
-            acc.y += w1 * x.y;
-            acc.z += w0 * x.z;
-            acc.w += w1 * x.w;
-        };
-        if (d.last - d.first < kFewParts) {  // (uniform) every load at once
-            float4 v[kFewParts], x[kFewParts];
+        const bool need = mine.first < mine.last && mine.first >= 0 &&
+                          mine.last < kMaxCtas * kWarps && mine.first_slot >> 1 == mine.first;
+        unsigned todo = __ballot_sync(0xffffffffu, need);
+        while (todo) {  // the same in every warp
+            const int k0 = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int row = (int)(r0 + (long long)k0 * gridDim.x);
+            const int first = __shfl_sync(0xffffffffu, mine.first, k0);
+            const int last = __shfl_sync(0xffffffffu, mine.last, k0);
+            const int first_slot = __shfl_sync(0xffffffffu, mine.first_slot, k0);
+            auto slot_of = [&](int c) { return (size_t)(c == first ? first_slot : 2 * c); };
+            float4 run = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);  // m, l of two heads
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float a0 = 0.f, a1 = 0.f;  // what exponents are taken against: m, 0 where -inf
+            // joins (m, l, o) v, x into the running ones
+            auto add = [&](const float4& v, const float4& x) {
+                const float w0 = fast_exp2(v.x - a0), w1 = fast_exp2(v.z - a1);
+                run.y = fmaf(w0, v.y, run.y);
+                run.w = fmaf(w1, v.w, run.w);
+                acc.x = fmaf(w0, x.x, acc.x);
+                acc.y = fmaf(w1, x.y, acc.y);
+                acc.z = fmaf(w0, x.z, acc.z);
+                acc.w = fmaf(w1, x.w, acc.w);
+            };
+            // raises the running maxima to m0, m1 at least
+            auto raise = [&](float m0, float m1) {
+                m0 = fmaxf(run.x, m0);
+                m1 = fmaxf(run.z, m1);
+                a0 = m0 == -INFINITY ? 0.f : m0;
+                a1 = m1 == -INFINITY ? 0.f : m1;
+                const float w0 = fast_exp2(run.x - a0), w1 = fast_exp2(run.z - a1);
+                run = make_float4(m0, run.y * w0, m1, run.w * w1);
+                acc = make_float4(acc.x * w0, acc.y * w1, acc.z * w0, acc.w * w1);
+            };
+            for (int c = first + team; has && c <= last; c += kTeams * kBatch) {
+                float4 v[kBatch], x[kBatch];
+                float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < kFewParts; ++k) {
-                const bool here = has && d.first + k <= d.last;
-                v[k] = here ? ml_of(d.first + k) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-                x[k] = here ? o_of(d.first + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+                for (int k = 0; k < kBatch; ++k) {
+                    const int part = c + k * kTeams;
+                    v[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (part <= last) {
+                        const size_t at = slot_of(part) * HPS + e;
+                        v[k] = *reinterpret_cast<const float4*>(ml + at * kMaxGroup + 2 * tig);
+                        x[k] = o[(at * KS + i) * 32 + lane];
+                    }
+                }
 #pragma unroll
-            for (int k = 0; k < kFewParts; ++k) {
-                M0 = fmaxf(M0, v[k].x);
-                M1 = fmaxf(M1, v[k].z);
-            }
-            if (M0 == -INFINITY) M0 = 0.f;
-            if (M1 == -INFINITY) M1 = 0.f;
+                for (int k = 0; k < kBatch; ++k) {
+                    m0 = fmaxf(m0, v[k].x);
+                    m1 = fmaxf(m1, v[k].z);
+                }
+                raise(m0, m1);
 #pragma unroll
-            for (int k = 0; k < kFewParts; ++k) add(v[k], x[k]);
-        } else {
-            for (int c = d.first + gid; has && c <= d.last; c += 8) {
-                const float4 v = ml_of(c);
-                M0 = fmaxf(M0, v.x);
-                M1 = fmaxf(M1, v.z);
+                for (int k = 0; k < kBatch; ++k) add(v[k], x[k]);
             }
+            if constexpr (kTeams > 1) {
+                __syncthreads();  // (the last row's have been read)
+                sm_ml[warp * 32 + lane] = run;
+                sm_acc[warp * 32 + lane] = acc;
+                __syncthreads();
+                if (team > 0) continue;
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, off));
-                M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, off));
+                for (int u = 1; u < kTeams; ++u) {
+                    const float4 v = sm_ml[(u * F + f) * 32 + lane];
+                    const float4 x = sm_acc[(u * F + f) * 32 + lane];
+                    raise(v.x, v.z);
+                    add(v, x);
+                }
             }
-            if (M0 == -INFINITY) M0 = 0.f;
-            if (M1 == -INFINITY) M1 = 0.f;
-            if (has) {
-#pragma unroll 8
-                for (int c = d.first; c <= d.last; ++c) add(ml_of(c), o_of(c));
-            }
+            const float inv0 = run.y != 0.f ? 1.f / run.y : 0.f;
+            const float inv1 = run.w != 0.f ? 1.f / run.w : 0.f;
+            const int s = row / HG, hg = row - s * HG;
+            T* head0 =
+                static_cast<T*>(out) + ((size_t)s * num_q_heads + (size_t)(hg * HPS + e) * g) * D;
+            store_fragment(head0, D, 16 * i, g, acc.x, acc.y, acc.z, acc.w, inv0, inv1);
         }
-        const float inv0 = L0 != 0.f ? 1.f / L0 : 0.f, inv1 = L1 != 0.f ? 1.f / L1 : 0.f;
-        const int s = row / HG, hg = row - s * HG;
-        T* head0 = static_cast<T*>(out) + ((size_t)s * num_q_heads + (size_t)(hg * HPS + e) * g) * D;
-        store_fragment(head0, D, 16 * i, g, acc.x, acc.y, acc.z, acc.w, inv0, inv1);
     }
 }
 
@@ -667,12 +698,13 @@ pkv_status launch_scored(const ScoredParams& prm, const CUtensorMap& tmk, const 
     if (prm.rows_whole) return PKV_OK;
     const int rows = prm.num_seqs * (prm.num_kv_heads / HPS);
     cfg.gridDim = dim3((unsigned)std::min(rows, kJoinCtas));
-    cfg.blockDim = dim3(HPS * (D / 16) * 32);
     cfg.dynamicSmemBytes = 0;
-    return cuda_status(cudaLaunchKernelEx(&cfg, scored_join_kernel<T, D, HPS>,
-                                          (const RowParts*)prm.rows, (const float2*)prm.ml,
-                                          (const float4*)prm.o, prm.out, rows, prm.num_q_heads,
-                                          prm.group));
+    const bool many = rows <= kManyTeamRows;
+    cfg.blockDim = dim3((many ? kManyTeams : 1) * HPS * (D / 16) * 32);
+    return cuda_status(cudaLaunchKernelEx(
+        &cfg, many ? scored_join_kernel<T, D, HPS, kManyTeams> : scored_join_kernel<T, D, HPS, 1>,
+        (const RowParts*)prm.rows, (const float2*)prm.ml, (const float4*)prm.o, prm.out, rows,
+        prm.num_q_heads, prm.group));
 }
 
 template <typename T, int D, int HPS>

@@ -348,3 +348,24 @@ def test_pools_past_two_to_the_31_elements(cuda_device):
     inp = dict(q=torch.randn(1, 16, D, device=dev).to(bf), k_cache=kc, v_cache=vc, tables=[ids],
                lens=[n], starts=None, window=0)
     check(inp, n, 0.1, softcap=20.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hkv,D", [(1, 128), (2, 64), (40, 64)])
+def test_parts_whose_scores_are_all_minus_infinity(cuda_device, Hkv, D):
+    """Keys that are seen with a score of -inf weigh nothing, whole parts of them in
+    front of a far lower but finite maximum too: as though the keys started later."""
+    lens = [2900, 2500, 700, 1] + [90] * 8
+    inp = make(cuda_device, lens, 2 * Hkv, Hkv, D, f16, seed=D + Hkv)
+    inp["q"][:, :, 0] = 4.0
+    later = []
+    for s, n in enumerate(lens):
+        later.append(n * 2 // 3)
+        for t in range(0, n, BS):
+            block = inp["k_cache"][inp["tables"][s][t // BS]]
+            block[:, :, 0] = -600.0
+            block[:max(0, min(BS, later[-1] - t)), :, 0] = -float("inf")
+    got = run(inp, 2900, 0.125)
+    want, tol = attention(inp["q"], inp["k_cache"], inp["v_cache"], inp["tables"], lens, None, 0.125,
+                          starts=later)
+    assert_close(got, want, tol)
