@@ -26,10 +26,14 @@ struct ScoreMods {
 constexpr float kScoreLog2e = 1.4426950408889634f;
 
 // tanh(x) / x as polynomials in x^2, fitted here by iterated weighted least
-// squares to the smallest largest relative error: four terms for |x| <= 0.5
-// (5.5e-7) and three for |x| <= 0.25 (4.0e-7).
-constexpr int kTanhTerms = 4, kTanhFew = 3;
-constexpr float kTanhRange = 0.5f, kTanhFewRange = 0.25f;
+// squares to the smallest largest relative error: eight terms for |x| <= 1.25
+// (8e-8, 2e-7 with their roundings), four for |x| <= 0.5 (5.5e-7) and three for
+// |x| <= 0.25 (4.0e-7).
+constexpr int kTanhWide = 8, kTanhTerms = 4, kTanhFew = 3;
+constexpr float kTanhWideRange = 1.25f, kTanhRange = 0.5f, kTanhFewRange = 0.25f;
+constexpr float kTanh8[kTanhWide] = {0.99999994f,   -0.333326995f,  0.133245066f,  -0.0534903146f,
+                                     0.0205571186f, -0.00679610018f, 0.00158808648f,
+                                     -0.000182592616f};
 constexpr float kTanh4[kTanhTerms] = {0.999999456f, -0.333263179f, 0.131902966f, -0.0444022261f};
 constexpr float kTanh3[kTanhFew] = {0.999999604f, -0.333219082f, 0.128416134f};
 

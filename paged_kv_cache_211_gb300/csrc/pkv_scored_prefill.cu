@@ -7,8 +7,8 @@
 // cap, bias and exp2.  With a cap the scores, not the products, bound it: tanh as
 // exp2 and a reciprocal makes three special functions a score, with the
 // softmax's own exp2.  So scores within |z / cap| <= 0.5 take tanh from a
-// polynomial on the packed fp32 pipe instead (a warp's 64 keys at a time), and
-// only the others the special-function pipe.
+// polynomial on the packed fp32 pipe instead (a warp's 64 keys at a time, four
+// terms; eight up to 1.25), and only the others the special-function pipe.
 //
 // Work item: one sequence, one KV head, a pair of 128-row tiles A and B (256
 // consecutive (query token, query head) rows) and, where items are few, one of
@@ -84,8 +84,8 @@ struct PrefillScored {
     int sorted;            // deal the items that hold rows, by their number of key tiles
     // the polynomials' terms, z = raw sum tanh_z[i] raw^2i, and the largest |raw
     // score| that each serves (negative: none)
-    float tanh_z[kTanhTerms], tanh_few[kTanhFew];
-    float tanh_limit, tanh_few_limit;
+    float tanh_z[kTanhTerms], tanh_few[kTanhFew], tanh_wide[kTanhWide];
+    float tanh_limit, tanh_few_limit, tanh_wide_limit;
     // partials of split items: row = ((base item) * splits + split) * kPair + row of the pair
     float* ws_m;
     float* ws_l;
@@ -423,7 +423,9 @@ __device__ __noinline__ void redo_rows(const PrefillScored& p, Item it, int row0
 
 // Raw scores to capped base-2 scores z = cap' tanh(raw cap_in), cap' = cap
 // log2(e).  Where the whole warp's scores allow it z is raw times a polynomial
-// in raw^2, two scores an instruction; else cap_score.
+// in raw^2, two scores an instruction; else cap_score.  (The prompts above with a
+// cap of 10, whose scores reach it: 351 us with the eight terms, 398 without;
+// fp16 385 and 468.)
 // top: the largest |raw score|.
 __device__ __forceinline__ float largest(const float (&sc)[kHalf]) {
     float top[4] = {0.f, 0.f, 0.f, 0.f};
@@ -432,29 +434,32 @@ __device__ __forceinline__ float largest(const float (&sc)[kHalf]) {
         top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], fabsf(sc[c]), fabsf(sc[c + 1]));
     return max3(fmaxf(top[0], top[1]), top[2], top[3]);
 }
+template <int N>
+__device__ __forceinline__ void cap_by_terms(const float* terms, float (&sc)[kHalf]) {
+#pragma unroll
+    for (int e0 = 0; e0 < kHalf; e0 += 8) {  // four independent chains at a time
+        uint64_t x[4], v[4], y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            x[u] = f2(sc[e0 + 2 * u], sc[e0 + 2 * u + 1]);
+            v[u] = f2_mul(x[u], x[u]);
+            y[u] = f2(terms[N - 1], terms[N - 1]);
+        }
+#pragma unroll
+        for (int i = N - 2; i >= 0; --i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[u], f2(terms[i], terms[i]));
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            f2_split(f2_mul(x[u], y[u]), sc[e0 + 2 * u], sc[e0 + 2 * u + 1]);
+    }
+}
 template <bool kSmallCap>
 __device__ __forceinline__ void cap_to_z(const PrefillScored& p, float (&sc)[kHalf], float top) {
     if (__all_sync(0xffffffffu, top <= p.tanh_limit)) {
-        const uint64_t c3 = f2(p.tanh_z[3], p.tanh_z[3]), c2 = f2(p.tanh_z[2], p.tanh_z[2]);
-        const uint64_t c1 = f2(p.tanh_z[1], p.tanh_z[1]), c0 = f2(p.tanh_z[0], p.tanh_z[0]);
-#pragma unroll
-        for (int e0 = 0; e0 < kHalf; e0 += 8) {  // four independent chains at a time
-            uint64_t x[4], v[4], y[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                x[u] = f2(sc[e0 + 2 * u], sc[e0 + 2 * u + 1]);
-                v[u] = f2_mul(x[u], x[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = f2_fma(c3, v[u], c2);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[u], c1);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[u] = f2_fma(y[u], v[u], c0);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                f2_split(f2_mul(x[u], y[u]), sc[e0 + 2 * u], sc[e0 + 2 * u + 1]);
-        }
+        cap_by_terms<kTanhTerms>(p.tanh_z, sc);
+    } else if (__all_sync(0xffffffffu, top <= p.tanh_wide_limit)) {
+        cap_by_terms<kTanhWide>(p.tanh_wide, sc);
     } else {
         // score by score: one large score (a hidden one's leftovers in shared memory
         // even) must not cost its neighbours near zero their relative error.  Under
@@ -902,11 +907,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t mul2 = f2(mul, mul);
                         if (__all_sync(0xffffffffu, key0 + kHalf - 1 <= pos)) {
                             const float base = slope2 * (float)(key0 - pos);
+                            const uint64_t step2 = f2(2.f * slope2, 2.f * slope2);
 #pragma unroll
-                            for (int c = 0; c < kHalf; c += 2) {
-                                const uint64_t bb = f2(fmaf(slope2, (float)c, base),
-                                                       fmaf(slope2, (float)(c + 1), base));
-                                f2_split(f2_fma(f2(sc[c], sc[c + 1]), mul2, bb), sc[c], sc[c + 1]);
+                            for (int c0 = 0; c0 < kHalf; c0 += 8) {
+                                // (exact products for a pair, then at most three steps)
+                                uint64_t bb = f2(fmaf(slope2, (float)c0, base),
+                                                 fmaf(slope2, (float)(c0 + 1), base));
+#pragma unroll
+                                for (int c = c0; c < c0 + 8; c += 2) {
+                                    f2_split(f2_fma(f2(sc[c], sc[c + 1]), mul2, bb), sc[c], sc[c + 1]);
+                                    if (c < c0 + 6) bb = f2_add(bb, step2);
+                                }
                             }
                         } else {
 #pragma unroll
@@ -1370,7 +1381,7 @@ pkv_status paged_attention_prefill_scored(
     prm.sorted = pl.items * pl.splits > ctas && entries <= pkv::kSortMax &&
                  pl.items * pl.splits <= (long long)pkv::kItemCache * ctas;
     // z = cap' x (tanh(x) / x) with x = raw cap_in: the terms in raw^2, times cap' cap_in
-    prm.tanh_limit = prm.tanh_few_limit = -1.f;
+    prm.tanh_limit = prm.tanh_few_limit = prm.tanh_wide_limit = -1.f;
     if (softcap > 0.f && scale != 0.f) {
         const float in = std::fabs(prm.mods.cap_in);
         float range = pkv::scaled_terms(pkv::kTanh4, pkv::kTanhTerms, pkv::kTanhRange, prm.mods,
@@ -1387,6 +1398,9 @@ pkv_status paged_attention_prefill_scored(
         const float few = pkv::scaled_terms(pkv::kTanh3, pkv::kTanhFew, pkv::kTanhFewRange,
                                             prm.mods, prm.tanh_few);
         if (few > 0.f) prm.tanh_few_limit = std::min(few / in, 1e18f);
+        const float wide = pkv::scaled_terms(pkv::kTanh8, pkv::kTanhWide, pkv::kTanhWideRange,
+                                             prm.mods, prm.tanh_wide);
+        if (wide > 0.f) prm.tanh_wide_limit = std::min(wide / in, 1e18f);
     }
     const pkv::Workspace ws =
         pkv::ws_layout(pl.splits > 1 ? pl.items * pl.splits * pkv::kPair : 0, head_dim);

@@ -233,6 +233,17 @@ def test_extreme_scores(cuda_device, scale, cap, q_std):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [bf, f16])
+@pytest.mark.parametrize("cap", [60.0, 40.0, 24.0, 12.0, 7.5, 6.0, 4.0])
+@pytest.mark.parametrize("sign,bias", [(1, False), (-1, False), (1, True)])
+def test_scores_at_every_share_of_the_cap(cuda_device, dtype, cap, sign, bias):
+    """Largest scores from a sixth of the cap to several times it: tanh has a form for
+    each range, chosen for a warp's scores at a time."""
+    inp = make(cuda_device, [300, 130], [300, 700], 8, 2, 128, dtype, seed=11, q_std=2.0)
+    check(inp, sign * 128 ** -0.5, softcap=cap, slopes=slopes_of(8, cuda_device) if bias else None)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,scale,cap", [(bf, 0.1, 1e6), (f16, 0.1, 1e5), (bf, 0.1, 50.0)])
 @pytest.mark.parametrize("reps", [1, 30])
 def test_large_scores_leave_small_ones_exact(cuda_device, dtype, scale, cap, reps):
