@@ -500,6 +500,14 @@ pkv_status paged_attention_prefill_scored(
     const int32_t* prefix_lens, void* out, void* workspace, size_t workspace_bytes,
     pkv_dtype dtype, pkv_stream_t stream);
 
+/* The rotary writes and the attention with modified scores for bindings that pay
+ * for each argument: `slots` is a host array of one 8-byte slot per argument, in
+ * order: a pointer, an int64 for an integer or enum, a double for a float. */
+pkv_status paged_kv_rope_write_packed(const void* slots);
+pkv_status paged_kv_rope_write_new_tokens_packed(const void* slots);
+pkv_status paged_attention_decode_scored_packed(const void* slots);
+pkv_status paged_attention_prefill_scored_packed(const void* slots);
+
 /* Chunked-prefill attention over the paged cache ([P2] 使用教程 step 4 and
  * 核心亮点: a self-written FlashAttention serves the prefill stage; [P3]
  * §关键工程决策 item 2: prefill chunks are batched with decode).  Sequence s

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -127,7 +128,17 @@ _SIGS = {
     "paged_attention_prefill_scored": ([_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i,
                                         _i, _f, _f, _vp, _i, _vp, _vp, _vp, _vp, _sz, _i, _vp],
                                        _i),
+    "paged_kv_rope_write_packed": ([ctypes.c_char_p], _i),
+    "paged_kv_rope_write_new_tokens_packed": ([ctypes.c_char_p], _i),
+    "paged_attention_decode_scored_packed": ([ctypes.c_char_p], _i),
+    "paged_attention_prefill_scored_packed": ([ctypes.c_char_p], _i),
 }
+# How each of their calls is packed: 8-byte slots, pointers (addresses, 0 for none),
+# integers and floats
+_SLOTS = {name: struct.Struct("=" + "".join({_vp: "Q", _f: "d"}.get(t, "q")
+                                            for t in _SIGS[name][0])).pack
+          for name in ("paged_kv_rope_write", "paged_kv_rope_write_new_tokens",
+                       "paged_attention_decode_scored", "paged_attention_prefill_scored")}
 
 
 def lib() -> ctypes.CDLL:
@@ -554,13 +565,13 @@ def paged_kv_rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1
 
 
 def _pointers(*named):
-    """Device pointers of (name, contiguous tensor or None) pairs, all on the current
-    CUDA device (where the kernels launch)."""
+    """Device addresses of (name, contiguous tensor or None) pairs, all on the current
+    CUDA device (where the kernels launch); 0 for None."""
     dev = named[0][1].get_device()
     ptrs = []
     for name, t in named:
         if t is None:
-            ptrs.append(None)
+            ptrs.append(0)
             continue
         if t.get_device() != dev or dev < 0:
             _refuse_device(name, t)
@@ -579,11 +590,11 @@ def _refuse_device(name, t):
                      f"cuda:{torch.cuda.current_device()}")
 
 
-def _stream_handle(stream):
-    """_stream, without making a Stream object for the current one."""
+def _stream_handle(stream) -> int:
+    """_stream's address, without making a Stream object for the current one."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return _stream(stream)
+    return _stream(stream).value or 0
 
 
 def _rows(name: str, t: torch.Tensor, dev: int):
@@ -628,13 +639,14 @@ def paged_kv_rope_write(q, k_new, v_new, k_cache, v_cache, positions, slot_mappi
     dev = q_out.get_device()
     (qp, qs), (kp, ks) = _rows("q", q, dev), _rows("k_new", k_new, dev)
     vp, vs = _rows("v_new", v_new, dev)
-    out, kc, vc, pos, slots, freq = _pointers(
+    out, kc, vc, pos, sm, freq = _pointers(
         ("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache), ("positions", positions),
         ("slot_mapping", slot_mapping), ("inv_freq", inv_freq))
-    _check("paged_kv_rope_write", lib().paged_kv_rope_write(
-        qp, kp, vp, qs, ks, vs, pos, slots, freq, float(rope_scale), T, Hq, Hkv, D,
+    packed = _SLOTS["paged_kv_rope_write"](
+        qp, kp, vp, qs, ks, vs, pos, sm, freq, float(rope_scale), T, Hq, Hkv, D,
         2 * inv_freq.shape[0], 1 if interleaved else 0, NB, out, kc, vc, _dtype_code(q),
-        _stream_handle(stream)))
+        _stream_handle(stream))
+    _check("paged_kv_rope_write", lib().paged_kv_rope_write_packed(packed))
     return q_out
 
 
@@ -648,14 +660,15 @@ def paged_kv_rope_write_new_tokens(q, k_new, v_new, k_cache, v_cache, block_tabl
     dev = q_out.get_device()
     (qp, qs), (kp, ks) = _rows("q", q, dev), _rows("k_new", k_new, dev)
     vp, vs = _rows("v_new", v_new, dev)
-    out, kc, vc, bt, cl, freq, slots = _pointers(
+    out, kc, vc, bt, cl, freq, sm = _pointers(
         ("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache),
         ("block_tables", block_tables), ("context_lens", context_lens), ("inv_freq", inv_freq),
         ("slot_mapping_out", slot_mapping_out))
-    _check("paged_kv_rope_write_new_tokens", lib().paged_kv_rope_write_new_tokens(
+    packed = _SLOTS["paged_kv_rope_write_new_tokens"](
         qp, kp, vp, qs, ks, vs, bt, block_tables.shape[1], cl, freq, float(rope_scale), B, Hq, Hkv, D,
-        2 * inv_freq.shape[0], 1 if interleaved else 0, NB, out, kc, vc, slots, _dtype_code(q),
-        _stream_handle(stream)))
+        2 * inv_freq.shape[0], 1 if interleaved else 0, NB, out, kc, vc, sm, _dtype_code(q),
+        _stream_handle(stream))
+    _check("paged_kv_rope_write_new_tokens", lib().paged_kv_rope_write_new_tokens_packed(packed))
     return q_out
 
 
@@ -702,11 +715,12 @@ def paged_attention_decode_scored(q, k_cache, v_cache, block_tables, context_len
         ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
         ("context_lens", context_lens), ("out", out), ("workspace", workspace),
         ("alibi_slopes", alibi_slopes), ("key_starts", key_starts))
-    _check("paged_attention_decode_scored", lib().paged_attention_decode_scored(
+    packed = _SLOTS["paged_attention_decode_scored"](
         qp, kc, vc, bt, block_tables.shape[1], cl, _int32(max_context_len, "max_context_len"), B,
         Hq, Hkv, D, NB, float(scale), float(softcap), slopes, _int32(window, "window"), starts,
         op, ws, workspace.numel() * workspace.element_size(), _dtype_code(q),
-        _stream_handle(stream)))
+        _stream_handle(stream))
+    _check("paged_attention_decode_scored", lib().paged_attention_decode_scored_packed(packed))
     return out
 
 
@@ -745,11 +759,12 @@ def paged_attention_prefill_scored(q, k_cache, v_cache, block_tables, context_le
         ("context_lens", context_lens), ("cu_q_lens", cu_q_lens), ("out", out),
         ("workspace", workspace), ("alibi_slopes", alibi_slopes), ("key_starts", key_starts),
         ("prefix_lens", prefix_lens))
-    _check("paged_attention_prefill_scored", lib().paged_attention_prefill_scored(
+    packed = _SLOTS["paged_attention_prefill_scored"](
         qp, kc, vc, bt, block_tables.shape[1], cl, cu, B, _int32(max_q_len, "max_q_len"), R, Hq,
         Hkv, D, NB, float(scale), float(softcap), slopes, _int32(window, "window"), starts,
         prefixes, op, ws,
-        workspace.numel() * workspace.element_size(), _dtype_code(q), _stream_handle(stream)))
+        workspace.numel() * workspace.element_size(), _dtype_code(q), _stream_handle(stream))
+    _check("paged_attention_prefill_scored", lib().paged_attention_prefill_scored_packed(packed))
     return out
 
 

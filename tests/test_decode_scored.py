@@ -42,13 +42,16 @@ def test_decode_scored_refuses(over, msg):
         pkv.paged_attention_decode_scored(**_cpu_args(**over))
 
 
-def _c_call(**over):
+def _c_call(entry="paged_attention_decode_scored", **over):
     a = dict(q=1 << 20, k_cache=2 << 20, v_cache=3 << 20, block_tables=4 << 20,
              max_blocks_per_seq=4, context_lens=5 << 20, max_context_len=64, num_seqs=2,
              num_q_heads=8, num_kv_heads=2, head_dim=64, num_blocks=8, scale=0.1, softcap=0.0,
              alibi_slopes=None, window=0, key_starts=None, out=6 << 20, workspace=7 << 20,
              workspace_bytes=1 << 30, dtype=1, stream=None)
     a.update(over)
+    if entry.endswith("_packed"):
+        slots = pkv._SLOTS[entry[:-7]](*(0 if v is None else v for v in a.values()))
+        return getattr(pkv.lib(), entry)(slots)
     return pkv.lib().paged_attention_decode_scored(*a.values())
 
 
@@ -65,6 +68,25 @@ def _c_call(**over):
 ])
 def test_decode_scored_c_statuses(over, status):
     assert _c_call(**over) == status
+
+
+@pytest.mark.parametrize("over", [{}, dict(q=None), dict(scale=float("nan")), dict(softcap=-1.0),
+                                  dict(num_q_heads=18), dict(workspace_bytes=1000),
+                                  dict(num_seqs=0), dict(dtype=3), dict(out=1 << 20)])
+def test_packed_arguments_mean_the_same(over):
+    """One array of 8-byte slots for the argument list."""
+    base = dict(workspace_bytes=0)    # (a refusal either way: no kernel runs)
+    packed = _c_call(entry="paged_attention_decode_scored_packed", **{**base, **over})
+    assert packed == _c_call(**{**base, **over})
+
+
+def test_packed_integers_are_not_cut():
+    for name in ("num_seqs", "max_context_len", "window", "dtype", "workspace_bytes"):
+        for wrong in (2 ** 32, -2 ** 32) if name != "workspace_bytes" else (-1,):
+            # (cut to 32 bits the call would only find its workspace too small)
+            assert _c_call(entry="paged_attention_decode_scored_packed",
+                           **{"workspace_bytes": 1000, name: wrong}) == 1
+    assert pkv.lib().paged_attention_decode_scored_packed(None) == 1
 
 
 def test_workspace_size():
