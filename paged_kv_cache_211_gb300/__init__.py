@@ -564,45 +564,41 @@ def paged_kv_rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1
     return inv_freq.to(device), rope_scale.value
 
 
-def _pointers(*named):
-    """Device addresses of (name, contiguous tensor or None) pairs, all on the current
-    CUDA device (where the kernels launch); 0 for None."""
-    dev = named[0][1].get_device()
-    ptrs = []
-    for name, t in named:
-        if t is None:
-            ptrs.append(0)
-            continue
-        if t.get_device() != dev or dev < 0:
-            _refuse_device(name, t)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous (pass a view of one layer's pool)")
-        ptrs.append(t.data_ptr())
-    if dev != torch.cuda.current_device():
-        _refuse_device(*named[0])
-    return ptrs
+def _addresses(names, *tensors):
+    """Device addresses of contiguous tensors (0 for None), and their device, which has
+    to be the current one (where the kernels launch)."""
+    dev = tensors[0].get_device()
+    at = [0 if t is None else t.data_ptr() if t.get_device() == dev and t.is_contiguous() else None
+          for t in tensors]
+    if None in at or dev < 0 or dev != torch.cuda.current_device():
+        for name, t in zip(names, tensors):
+            if t is not None:
+                _check_place(name, t)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous (pass a view of one layer's pool)")
+    return at, dev
 
 
-def _refuse_device(name, t):
+def _check_place(name, t):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    raise ValueError(f"{name} is on {t.device}; every tensor must be on the current device, "
-                     f"cuda:{torch.cuda.current_device()}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}; every tensor must be on the current device, "
+                         f"cuda:{torch.cuda.current_device()}")
 
 
-def _stream_handle(stream) -> int:
+def _stream_handle(stream, dev: int) -> int:
     """_stream's address, without making a Stream object for the current one."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return _stream(stream).value or 0
 
 
-def _rows(name: str, t: torch.Tensor, dev: int):
-    """Pointer and token stride of rows [T, heads, D] whose heads are packed (the
-    tokens may be spaced, as in a view of a wider projection's rows)."""
-    if t.get_device() != dev or dev < 0:
-        _refuse_device(name, t)
-    T, H, D = t.shape
+def _rows(name: str, t: torch.Tensor, T: int, H: int, D: int, dev: int):
+    """Address and token stride of rows [T, H, D] whose heads are packed (the tokens may
+    be spaced, as in a view of a wider projection's rows)."""
+    if t.get_device() != dev:
+        _check_place(name, t)
     st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name} must have contiguous heads (only the token stride is free)")
@@ -618,7 +614,10 @@ def _check_rope(q, k_new, v_new, k_cache, v_cache, inv_freq, q_out):
     NB, bs, Hkv, D2 = k_cache.shape
     if bs != BLOCK_SIZE or D2 != D or v_cache.shape != k_cache.shape:
         raise ValueError("pool shape must be [num_blocks, 16, num_kv_heads, head_dim]")
-    _check_new_rows(k_new, v_new, (T, Hkv, D), q.dtype)
+    dtype = q.dtype
+    if (k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape or k_new.dtype != dtype
+            or v_new.dtype != dtype):
+        raise ValueError(f"k_new/v_new must be shaped {(T, Hkv, D)} in q's dtype")
     _check_dtypes(q, k_cache, v_cache, q_out)
     if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or 2 * inv_freq.numel() > D:
         raise ValueError("inv_freq must be float32 [rotary_dim / 2], rotary_dim <= head_dim")
@@ -636,16 +635,16 @@ def paged_kv_rope_write(q, k_new, v_new, k_cache, v_cache, positions, slot_mappi
         raise ValueError("positions must be int32 [num_tokens]")
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be int64 [num_tokens]")
-    dev = q_out.get_device()
-    (qp, qs), (kp, ks) = _rows("q", q, dev), _rows("k_new", k_new, dev)
-    vp, vs = _rows("v_new", v_new, dev)
-    out, kc, vc, pos, sm, freq = _pointers(
-        ("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache), ("positions", positions),
-        ("slot_mapping", slot_mapping), ("inv_freq", inv_freq))
+    (out, kc, vc, pos, sm, freq), dev = _addresses(
+        ("q_out", "k_cache", "v_cache", "positions", "slot_mapping", "inv_freq"),
+        q_out, k_cache, v_cache, positions, slot_mapping, inv_freq)
+    qp, qs = _rows("q", q, T, Hq, D, dev)
+    kp, ks = _rows("k_new", k_new, T, Hkv, D, dev)
+    vp, vs = _rows("v_new", v_new, T, Hkv, D, dev)
     packed = _SLOTS["paged_kv_rope_write"](
         qp, kp, vp, qs, ks, vs, pos, sm, freq, float(rope_scale), T, Hq, Hkv, D,
         2 * inv_freq.shape[0], 1 if interleaved else 0, NB, out, kc, vc, _dtype_code(q),
-        _stream_handle(stream))
+        _stream_handle(stream, dev))
     _check("paged_kv_rope_write", lib().paged_kv_rope_write_packed(packed))
     return q_out
 
@@ -657,17 +656,17 @@ def paged_kv_rope_write_new_tokens(q, k_new, v_new, k_cache, v_cache, block_tabl
     B, Hq, Hkv, D, NB = _check_rope(q, k_new, v_new, k_cache, v_cache, inv_freq, q_out)
     _check_tables(block_tables, context_lens, B)
     _check_slots(slot_mapping_out, B, "slot_mapping_out")
-    dev = q_out.get_device()
-    (qp, qs), (kp, ks) = _rows("q", q, dev), _rows("k_new", k_new, dev)
-    vp, vs = _rows("v_new", v_new, dev)
-    out, kc, vc, bt, cl, freq, sm = _pointers(
-        ("q_out", q_out), ("k_cache", k_cache), ("v_cache", v_cache),
-        ("block_tables", block_tables), ("context_lens", context_lens), ("inv_freq", inv_freq),
-        ("slot_mapping_out", slot_mapping_out))
+    (out, kc, vc, bt, cl, freq, sm), dev = _addresses(
+        ("q_out", "k_cache", "v_cache", "block_tables", "context_lens", "inv_freq",
+         "slot_mapping_out"),
+        q_out, k_cache, v_cache, block_tables, context_lens, inv_freq, slot_mapping_out)
+    qp, qs = _rows("q", q, B, Hq, D, dev)
+    kp, ks = _rows("k_new", k_new, B, Hkv, D, dev)
+    vp, vs = _rows("v_new", v_new, B, Hkv, D, dev)
     packed = _SLOTS["paged_kv_rope_write_new_tokens"](
         qp, kp, vp, qs, ks, vs, bt, block_tables.shape[1], cl, freq, float(rope_scale), B, Hq, Hkv, D,
         2 * inv_freq.shape[0], 1 if interleaved else 0, NB, out, kc, vc, sm, _dtype_code(q),
-        _stream_handle(stream))
+        _stream_handle(stream, dev))
     _check("paged_kv_rope_write_new_tokens", lib().paged_kv_rope_write_new_tokens_packed(packed))
     return q_out
 
@@ -711,15 +710,15 @@ def paged_attention_decode_scored(q, k_cache, v_cache, block_tables, context_len
     B, Hq, Hkv, D, NB = _check_decode_shapes(q, k_cache, v_cache, block_tables, context_lens,
                                              out)
     _check_score_mods(Hq, B, alibi_slopes, key_starts=key_starts)
-    qp, kc, vc, bt, cl, op, ws, slopes, starts = _pointers(
-        ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
-        ("context_lens", context_lens), ("out", out), ("workspace", workspace),
-        ("alibi_slopes", alibi_slopes), ("key_starts", key_starts))
+    (qp, kc, vc, bt, cl, op, ws, slopes, starts), dev = _addresses(
+        ("q", "k_cache", "v_cache", "block_tables", "context_lens", "out", "workspace",
+         "alibi_slopes", "key_starts"),
+        q, k_cache, v_cache, block_tables, context_lens, out, workspace, alibi_slopes, key_starts)
     packed = _SLOTS["paged_attention_decode_scored"](
         qp, kc, vc, bt, block_tables.shape[1], cl, _int32(max_context_len, "max_context_len"), B,
         Hq, Hkv, D, NB, float(scale), float(softcap), slopes, _int32(window, "window"), starts,
         op, ws, workspace.numel() * workspace.element_size(), _dtype_code(q),
-        _stream_handle(stream))
+        _stream_handle(stream, dev))
     _check("paged_attention_decode_scored", lib().paged_attention_decode_scored_packed(packed))
     return out
 
@@ -754,16 +753,16 @@ def paged_attention_prefill_scored(q, k_cache, v_cache, block_tables, context_le
         raise ValueError("cu_q_lens must be int32 [num_seqs + 1]")
     _check_dtypes(q, k_cache, v_cache, out)
     _check_score_mods(Hq, B, alibi_slopes, key_starts=key_starts, prefix_lens=prefix_lens)
-    qp, kc, vc, bt, cl, cu, op, ws, slopes, starts, prefixes = _pointers(
-        ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
-        ("context_lens", context_lens), ("cu_q_lens", cu_q_lens), ("out", out),
-        ("workspace", workspace), ("alibi_slopes", alibi_slopes), ("key_starts", key_starts),
-        ("prefix_lens", prefix_lens))
+    (qp, kc, vc, bt, cl, cu, op, ws, slopes, starts, prefixes), dev = _addresses(
+        ("q", "k_cache", "v_cache", "block_tables", "context_lens", "cu_q_lens", "out", "workspace",
+         "alibi_slopes", "key_starts", "prefix_lens"),
+        q, k_cache, v_cache, block_tables, context_lens, cu_q_lens, out, workspace, alibi_slopes,
+        key_starts, prefix_lens)
     packed = _SLOTS["paged_attention_prefill_scored"](
         qp, kc, vc, bt, block_tables.shape[1], cl, cu, B, _int32(max_q_len, "max_q_len"), R, Hq,
         Hkv, D, NB, float(scale), float(softcap), slopes, _int32(window, "window"), starts,
         prefixes, op, ws,
-        workspace.numel() * workspace.element_size(), _dtype_code(q), _stream_handle(stream))
+        workspace.numel() * workspace.element_size(), _dtype_code(q), _stream_handle(stream, dev))
     _check("paged_attention_prefill_scored", lib().paged_attention_prefill_scored_packed(packed))
     return out
 
