@@ -39,9 +39,10 @@
  *    never dereferenced, the affected row is skipped or zero-filled, and a
  *    bit is set in the device status word (pkv_device_status).  No kernel
  *    traps, asserts or spins without a bound.
- *  - The decode partition pass, the merge pass and the host-input staging
- *    kernel are launched as programmatic dependents of the kernel before them
- *    on the stream, so their CTAs are scheduled while it drains.  Each waits
+ *  - The decode partition pass, the merge pass, the host-input staging kernel,
+ *    the rotary writes and the kernels of attention with modified scores are
+ *    launched as programmatic dependents of the kernel before them on the
+ *    stream, so their CTAs are scheduled while it drains.  Each waits
  *    for that kernel to complete (griddepcontrol.wait, which also makes its
  *    stores visible) before it reads or writes any caller memory, whatever
  *    that kernel is.  One exception, internal to a call: in
@@ -51,8 +52,9 @@
  *    is layer l - 1's, which touches none of them.  It waits before its
  *    first workspace write (layer l - 1's merge reads the workspace) and
  *    before it ends, so that it never completes before that kernel.  The
- *    TMA partition pass (after its prologue) and the merge pass (once its
- *    partition pass has finished) let the next kernel's CTAs be scheduled
+ *    TMA partition pass (after its prologue), the merge pass (once its
+ *    partition pass has finished), the rotary writes and the kernels of
+ *    attention with modified scores let the next kernel's CTAs be scheduled
  *    before they end; a dependent of another library must then wait for
  *    them (griddepcontrol.wait) before it reads their outputs, as
  *    programmatic dependent launch requires of any dependent.

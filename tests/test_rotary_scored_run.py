@@ -134,3 +134,66 @@ def test_prompt_then_decode(cuda_device, dtype, D, R, interleaved, window):
                                [1] * B)
             assert_close(out[layer], want, tol, f"step {i} layer {layer}")
     assert pkv.pkv_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_in_a_row_see_one_another(cuda_device, graph):
+    """Each call reads what the one in front of it wrote, and kernels are scheduled
+    before their predecessors end: the same bits as with a wait after every call."""
+    dev, dtype = cuda_device, torch.bfloat16
+    B, Hq, Hkv, D, n, rounds = 4, 4, 2, 128, 900, 12
+    MB = (n + BS - 1) // BS
+    gen = torch.Generator(device=dev).manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device=dev).to(dtype)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+    bt = torch.randperm(B * MB, generator=gen, device=dev).to(torch.int32).view(B, MB)
+    k0, v0, x0 = rnd(B * MB, BS, Hkv, D), rnd(B * MB, BS, Hkv, D), rnd(B, Hq, D)
+    lens, cu = i32([n, n - 1, n - 40, n]), i32(range(B + 1))
+    freq = pkv.paged_kv_rope_frequencies(D, device=dev)[0]
+    ws = [pkv.new_scored_workspace(B, Hq, Hkv, D, n, dev),
+          pkv.new_prefill_scored_workspace(B, 1, Hq, Hkv, D, dev),
+          pkv.new_workspace(B, Hq, D, n, dev)]
+    kc, vc, x = k0.clone(), v0.clone(), x0.clone()
+    qr, a, b = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+
+    def chain(after):
+        for _ in range(rounds):
+            pkv.paged_kv_rope_write_new_tokens(x, x[:, :Hkv], x[:, Hkv:], kc, vc, bt, lens, freq, qr)
+            after()
+            pkv.paged_attention_decode_scored(qr, kc, vc, bt, lens, n, 0.3, a, ws[0], softcap=90.0)
+            after()
+            pkv.paged_attention_prefill_scored(a, kc, vc, bt, lens, cu, 1, 0.3, b, ws[1],
+                                               window=500)
+            after()
+            pkv.paged_attention_decode(b, kc, vc, bt, lens, n, 0.3, a, ws[2])
+            after()
+            pkv.paged_attention_prefill_scored(a, kc, vc, bt, lens, cu, 1, 0.3, b, ws[1],
+                                               softcap=50.0)
+            after()
+            x.copy_(b * 8)
+            after()
+
+    def reset():
+        for t, t0 in ((kc, k0), (vc, v0), (x, x0)):
+            t.copy_(t0)
+        torch.cuda.synchronize()
+
+    chain(torch.cuda.synchronize)
+    want = [t.clone() for t in (kc, vc, x, a, b, qr)]
+    assert torch.isfinite(want[2]).all()
+    reset()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            chain(lambda: None)
+    for _ in range(5):
+        reset()
+        if graph:
+            g.replay()
+        else:
+            chain(lambda: None)
+        torch.cuda.synchronize()
+        for t, w in zip((kc, vc, x, a, b, qr), want):
+            assert torch.equal(t, w)
+    assert pkv.pkv_device_status() == 0
