@@ -31,7 +31,7 @@
 //
 // Measured: 32 sequences of 2048 to 32768 tokens, 32q/8kv heads of 128, bf16,
 // cap 50: 181 us, 6.2 TB/s of K and V (the first kernel alone 6.5 TB/s); a
-// 1000-token window over 256 sequences, 32q/4kv heads of 64: 50 us, 5.0 TB/s; 60
+// 1000-token window over 256 sequences, 32q/4kv heads of 64: 51 us, 4.9 TB/s; 60
 // sequences of 32 to 512 tokens, 16q/8kv heads of 128: 14.2 us, of which the
 // launch, the lengths and the first copies take 6 and the join 4.  Equal runs end
 // up to a tenth apart, by SM; handing their last eighth out as chunks made them

@@ -30,8 +30,8 @@
 // would still meet a zero weight: a row whose O is not finite is computed again,
 // by a plain loop over its own keys.  Every wait is bounded.
 //
-// Measured: 8 prompts of 2048 tokens, 32q/8kv heads of 128, bf16, cap 50: 266 us,
-// 1034 TFLOP/s of visible pairs.  The tensor pipe is active 46 % of the time, the
+// Measured: 8 prompts of 2048 tokens, 32q/8kv heads of 128, bf16, cap 50: 269 us,
+// 1022 TFLOP/s of visible pairs.  The tensor pipe is active 46 % of the time, the
 // fp32 pipe 35 %, the integer and min / max pipe 30 %, the special functions
 // 23 %: no pipe bounds it but the chain S -> weights -> P V -> next S of each
 // tile, which tensor memory leaves no room to double (O and S of two tiles fill
